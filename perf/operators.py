@@ -128,7 +128,7 @@ def _quantise(x):
     m = a.abs()
     code = ((m > 0.25).to(torch.uint8) + (m >= 0.75) + (m > 1.25) + (m >= 1.75) + (m > 2.5)
             + (m >= 3.5) + (m > 5.0))
-    code = (code + 8 * (a < 0)).flatten(-2)
+    code = (code + (a < 0).to(torch.uint8) * 8).flatten(-2)
     scales = (s.half().view(torch.int16) >> 7).to(torch.uint8)
     return code[..., 0::2] | (code[..., 1::2] << 4), scales
 
