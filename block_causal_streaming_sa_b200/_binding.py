@@ -25,6 +25,7 @@ SA_ERR_CUDA = 4
 SA_ERR_TIMEOUT = 5
 SA_ERR_RANGE = 6
 SA_ERR_BOUNDS = 7
+SA_ERR_FULL = 8
 SA_BUILD_DEVICE_CHECKS = 1
 SA_TIER_NOISY = 0
 SA_TIER_CLEAN = 1
@@ -33,6 +34,9 @@ SA_NOALLOC_MAX_KEY_BYTES = 64 << 20
 SA_PAYLOAD_FP8 = 0
 SA_PAYLOAD_BF16 = 1
 SA_IPC_HANDLE_BYTES = 64
+SA_DTYPE_BF16 = 0
+SA_DTYPE_FP16 = 1
+SA_KV4_LAST = -1
 
 
 class SaConfig(ctypes.Structure):
@@ -51,6 +55,25 @@ class SaConfig(ctypes.Structure):
     ]
 
 
+class SaKv4Cache(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int32),
+        ("kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("capacity", ctypes.c_int32),
+    ] + [(name, ctypes.c_void_p) for name in
+         ("k_codes", "v_codes", "k_scales", "v_scales", "pos", "weight", "seq", "status")]
+
+
+class SaRows(ctypes.Structure):
+    _fields_ = [
+        ("data", ctypes.c_void_p),
+        ("stride_b", ctypes.c_int64),
+        ("stride_t", ctypes.c_int64),
+        ("stride_h", ctypes.c_int64),
+    ]
+
+
 class SaError(RuntimeError):
     def __init__(self, status, message):
         super().__init__(f"{status_name(status)}: {message}")
@@ -62,6 +85,8 @@ _P = ctypes.c_void_p
 _I = ctypes.c_int
 _I32P = ctypes.POINTER(ctypes.c_int32)
 _CFGP = ctypes.POINTER(SaConfig)
+_KV4P = ctypes.POINTER(SaKv4Cache)
+_ROWSP = ctypes.POINTER(SaRows)
 
 _SIGNATURES = {
     "sa_validate_config": (_I, [_CFGP]),
@@ -100,6 +125,15 @@ _SIGNATURES = {
     "sa_ipc_handle": (_I, [_P, ctypes.c_char_p]),
     "sa_ipc_open": (_I, [ctypes.c_char_p, ctypes.POINTER(_P)]),
     "sa_ipc_close": (_I, [_P]),
+    "sa_kv4_reset": (_I, [_KV4P, _P]),
+    "sa_kv4_append": (_I, [_KV4P, _ROWSP, _ROWSP, _I, _I, _P, _I, _P]),
+    "sa_kv4_read": (_I, [_KV4P, _I, _ROWSP, _ROWSP, _I, _I, _P]),
+    "sa_kv4_attend_bytes": (ctypes.c_size_t, [_KV4P, _I, _I, _I]),
+    "sa_kv4_attend": (_I, [_KV4P, _ROWSP, _ROWSP, _I, _I, _I, _P, _I, ctypes.c_float, _P, _I, _P,
+                           ctypes.c_size_t, _P]),
+    "sa_kv4_evict_bytes": (ctypes.c_size_t, [_KV4P]),
+    "sa_kv4_evict": (_I, [_KV4P, _I, _I, _I, _P, ctypes.c_size_t, _P]),
+    "sa_kv4_get_status": (_I, [_KV4P, _P]),
     "sa_get_status": (_I, [_P, _P]),
     "sa_last_error": (ctypes.c_char_p, [_P]),
     "sa_status_string": (ctypes.c_char_p, [_I]),
@@ -355,3 +389,48 @@ def sa_ipc_alloc(nbytes):
 
 def sa_ipc_free(dev_ptr):
     _check(lib().sa_ipc_free(_P(dev_ptr)))
+
+
+# ---- 4-bit KV cache. cache: SaKv4Cache; K, V, Q, O: SaRows (None is passed as NULL).
+
+def _ref(struct):
+    return None if struct is None else ctypes.byref(struct)
+
+
+def sa_kv4_reset(cache, stream=0):
+    _check(lib().sa_kv4_reset(_ref(cache), stream or None))
+
+
+def sa_kv4_append(cache, K, V, dtype, T, counts=0, replace=False, stream=0):
+    _check(lib().sa_kv4_append(_ref(cache), _ref(K), _ref(V), dtype, T, counts or None,
+                               int(bool(replace)), stream or None))
+
+
+def sa_kv4_read(cache, first, K, V, dtype, T, stream=0):
+    _check(lib().sa_kv4_read(_ref(cache), first, _ref(K), _ref(V), dtype, T, stream or None))
+
+
+def sa_kv4_attend_bytes(cache, heads, T, add_weight=False):
+    """Workspace bytes of an attention (0 if the sizes are invalid)."""
+    return lib().sa_kv4_attend_bytes(_ref(cache), heads, T, int(bool(add_weight)))
+
+
+def sa_kv4_attend(cache, Q, O, dtype, heads, T, counts=0, causal=False, scale=0.0, lse=0,
+                  add_weight=False, workspace=0, workspace_bytes=0, stream=0):
+    _check(lib().sa_kv4_attend(_ref(cache), _ref(Q), _ref(O), dtype, heads, T, counts or None,
+                               int(bool(causal)), scale, lse or None, int(bool(add_weight)),
+                               workspace or None, workspace_bytes, stream or None))
+
+
+def sa_kv4_evict_bytes(cache):
+    """Workspace bytes of an eviction (0 if the sizes are invalid)."""
+    return lib().sa_kv4_evict_bytes(_ref(cache))
+
+
+def sa_kv4_evict(cache, keep, first=0, recent=0, workspace=0, workspace_bytes=0, stream=0):
+    _check(lib().sa_kv4_evict(_ref(cache), keep, first, recent, workspace or None,
+                              workspace_bytes, stream or None))
+
+
+def sa_kv4_get_status(cache, stream=0):
+    return lib().sa_kv4_get_status(_ref(cache), stream or None)

@@ -15,11 +15,13 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libsa.so")
 LIB_CHECKED = os.path.join(HERE, "libsa_checked.so")
 
+UNITS = ["sa_api.cu", "kv4_api.cu"]  # chunk cache and exchange; 4-bit cache
+
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-std=c++17", "-lineinfo",
     "-Xcompiler", "-fPIC,-fvisibility=hidden",
-    "-shared",
+    "-shared", "-t", "2",
 ]
 
 
@@ -40,7 +42,7 @@ def up_to_date(lib):
 def _compile(lib, extra, verbose):
     nvcc = os.environ.get("NVCC", "nvcc")
     cmd = [nvcc] + NVCC_FLAGS + extra + (["-Xptxas", "-v"] if verbose else []) + [
-        os.path.join(CSRC, "sa_api.cu"), "-o", lib + ".tmp"]
+        os.path.join(CSRC, f) for f in UNITS] + ["-o", lib + ".tmp"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if verbose or res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
@@ -50,7 +52,7 @@ def _compile(lib, extra, verbose):
 
 
 def build(force=False, verbose=False, checked=True):
-    """Compile csrc/sa_api.cu (which includes every kernel) into libsa.so and,
+    """Compile csrc/'s units (which include every kernel) into libsa.so and,
     with checked, into libsa_checked.so as well."""
     if force or not up_to_date(LIB):
         _compile(LIB, [], verbose)

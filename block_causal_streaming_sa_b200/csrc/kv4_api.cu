@@ -1,0 +1,351 @@
+// Host side of the 4-bit KV cache (include/sa.h: sa_kv4_*): argument checks,
+// workspace layout and kernel launches. Nothing is kept between calls.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <initializer_list>
+#include <string>
+
+#include "host_common.h"
+#include "kernels/kv4_attend_rows.cuh"
+#include "kernels/kv4_evict.cuh"
+#include "kernels/kv4_rows.cuh"
+
+using sa::aligned16;
+using sa::device_memory;
+using sa::g_error;
+using sa::Kv4;
+using sa::Kv4Rows;
+using sa::NvtxRange;
+
+namespace {
+
+constexpr int kMaxGridYZ = 65535;
+
+int refuse(int code, const std::string& why) {
+  g_error = "kv4: " + why;
+  return code;
+}
+
+size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+// Makes `device` current for the call's launches and puts the caller's back.
+class DeviceGuard {
+ public:
+  explicit DeviceGuard(int device) {
+    if (cudaGetDevice(&before_) != cudaSuccess) before_ = -1;
+    if (before_ >= 0 && device >= 0 && device != before_)
+      changed_ = cudaSetDevice(device) == cudaSuccess;
+  }
+  ~DeviceGuard() {
+    if (changed_) cudaSetDevice(before_);
+  }
+  DeviceGuard(const DeviceGuard&) = delete;
+  DeviceGuard& operator=(const DeviceGuard&) = delete;
+
+ private:
+  int before_ = -1;
+  bool changed_ = false;
+};
+
+int check_sizes(const sa_kv4_cache* c) {
+  if (c == nullptr) return refuse(SA_ERR_INVALID_ARG, "cache is NULL");
+  if (c->batch < 1 || c->kv_heads < 1 || c->capacity < 1)
+    return refuse(SA_ERR_INVALID_ARG, "batch, kv_heads and capacity must be >= 1");
+  if (c->head_dim != 64 && c->head_dim != 128)
+    return refuse(SA_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
+  if (c->capacity % 128 != 0)
+    return refuse(SA_ERR_INVALID_ARG, "capacity must be a multiple of 128");
+  if (c->batch > kMaxGridYZ || c->kv_heads > kMaxGridYZ ||
+      1LL * c->batch * c->kv_heads > (1LL << 24) || c->capacity > (1 << 30))
+    return refuse(SA_ERR_UNSUPPORTED, "too many sequences, heads or rows");
+  return SA_OK;
+}
+
+// Sizes, pointers and the device they lie on (-1: managed memory).
+int check_cache(const sa_kv4_cache* c, Kv4* out, int* device) {
+  if (int rc = check_sizes(c); rc != SA_OK) return rc;
+  const void* const ptr[8] = {c->k_codes, c->v_codes, c->k_scales, c->v_scales,
+                              c->pos,     c->weight,  c->seq,      c->status};
+  static const char* const name[8] = {"k_codes", "v_codes", "k_scales", "v_scales",
+                                      "pos",     "weight",  "seq",      "status"};
+  for (int i = 0; i < 8; ++i)
+    if (ptr[i] == nullptr || !aligned16(ptr[i]))
+      return refuse(SA_ERR_INVALID_ARG,
+                    std::string(name[i]) + " must be non-NULL and 16-byte aligned");
+  std::string why;
+  *device = -1;
+  cudaPointerAttributes a;
+  if (cudaPointerGetAttributes(&a, c->k_codes) == cudaSuccess) {
+    if (a.type == cudaMemoryTypeDevice) *device = a.device;
+  } else {
+    cudaGetLastError();
+  }
+  for (int i = 0; i < 8; ++i)
+    if (!device_memory(ptr[i], *device, name[i], &why)) return refuse(SA_ERR_INVALID_ARG, why);
+  out->B = c->batch;
+  out->H = c->kv_heads;
+  out->N = c->capacity;
+  out->k_codes = c->k_codes;
+  out->v_codes = c->v_codes;
+  out->k_scales = c->k_scales;
+  out->v_scales = c->v_scales;
+  out->pos = c->pos;
+  out->weight = c->weight;
+  out->seq = c->seq;
+  out->status = c->status;
+  return SA_OK;
+}
+
+// Rows [B, T, heads, D]; `written`: no two rows may overlap.
+int check_rows(const sa_rows* r, const char* name, int B, int T, int heads, int D, bool written,
+               int device, Kv4Rows* out) {
+  if (r == nullptr || (r->data == nullptr && T > 0) || !aligned16(r->data))
+    return refuse(SA_ERR_INVALID_ARG,
+                  std::string(name) + " must be non-NULL and 16-byte aligned");
+  for (int64_t s : {r->stride_b, r->stride_t, r->stride_h})
+    if (s < 0 || s % 8 != 0)
+      return refuse(SA_ERR_INVALID_ARG,
+                    std::string(name) + ": strides must be multiples of 8 and >= 0");
+  if (written && ((B > 1 && r->stride_b < D) || (T > 1 && r->stride_t < D) ||
+                  (heads > 1 && r->stride_h < D)))
+    return refuse(SA_ERR_INVALID_ARG, std::string(name) + ": rows that are written overlap");
+  std::string why;
+  if (!device_memory(r->data, device, name, &why)) return refuse(SA_ERR_INVALID_ARG, why);
+  out->data = r->data;
+  out->sb = r->stride_b;
+  out->st = r->stride_t;
+  out->sh = r->stride_h;
+  return SA_OK;
+}
+
+int check_call(int dtype, int T, int max_T, const int32_t* counts, int device) {
+  if (dtype != SA_DTYPE_BF16 && dtype != SA_DTYPE_FP16)
+    return refuse(SA_ERR_INVALID_ARG, "dtype must be SA_DTYPE_BF16 or SA_DTYPE_FP16");
+  if (T < 0) return refuse(SA_ERR_INVALID_ARG, "T must be >= 0");
+  if (T > max_T) return refuse(SA_ERR_UNSUPPORTED, "T is too large");
+  if (reinterpret_cast<uintptr_t>(counts) & 3u)
+    return refuse(SA_ERR_INVALID_ARG, "counts must be 4-byte aligned");
+  std::string why;
+  if (!device_memory(counts, device, "counts", &why)) return refuse(SA_ERR_INVALID_ARG, why);
+  return SA_OK;
+}
+
+int check_workspace(const void* ws, size_t bytes, size_t need, int device) {
+  if (need == 0) return SA_OK;
+  if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0 || bytes < need)
+    return refuse(SA_ERR_INVALID_ARG,
+                  "workspace must be 256-byte aligned and hold the bytes asked for");
+  std::string why;
+  if (!device_memory(ws, device, "workspace", &why)) return refuse(SA_ERR_INVALID_ARG, why);
+  return SA_OK;
+}
+
+int launched(const char* what) {
+  const cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) return SA_OK;
+  return refuse(SA_ERR_CUDA, std::string(what) + " launch: " + cudaGetErrorString(e));
+}
+
+constexpr int kMaxTokens = 1 << 24;
+
+int check_heads(const sa_kv4_cache* c, int heads, int T) {
+  if (heads < 1 || heads % c->kv_heads != 0)
+    return refuse(SA_ERR_INVALID_ARG, "heads must be a multiple of kv_heads");
+  if (heads > kMaxGridYZ || 1LL * (heads / c->kv_heads) * T > (1LL << 30))
+    return refuse(SA_ERR_UNSUPPORTED, "too many query rows");
+  return SA_OK;
+}
+
+size_t attend_bytes(const sa_kv4_cache* c, int heads, int T) {
+  return align_up(static_cast<size_t>(c->batch) * heads * T * sizeof(float), 256);
+}
+
+size_t evict_bytes(const sa_kv4_cache* c) {
+  const size_t planes = static_cast<size_t>(c->batch) * c->kv_heads;
+  return align_up(planes * 4, 256) + planes * c->capacity * 4;
+}
+
+}  // namespace
+
+extern "C" {
+
+SA_API int sa_kv4_reset(const sa_kv4_cache* c, sa_stream stream) {
+  NvtxRange range_("sa_kv4_reset");
+  Kv4 k;
+  int device;
+  if (int rc = check_cache(c, &k, &device); rc != SA_OK) return rc;
+  DeviceGuard guard(device);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaMemsetAsync(k.seq, 0, sizeof(int32_t) * 4 * k.B, s);
+  if (e == cudaSuccess) e = cudaMemsetAsync(k.status, 0, 16, s);
+  if (e != cudaSuccess)
+    return refuse(SA_ERR_CUDA, std::string("reset: ") + cudaGetErrorString(e));
+  return SA_OK;
+}
+
+SA_API int sa_kv4_append(const sa_kv4_cache* c, const sa_rows* K, const sa_rows* V, int dtype,
+                         int T, const int32_t* counts, int replace, sa_stream stream) {
+  NvtxRange range_("sa_kv4_append");
+  sa::Kv4AppendParams p;
+  int device;
+  if (int rc = check_cache(c, &p.c, &device); rc != SA_OK) return rc;
+  if (int rc = check_call(dtype, T, kMaxTokens, counts, device); rc != SA_OK) return rc;
+  const int D = c->head_dim;
+  if (int rc = check_rows(K, "K", p.c.B, T, p.c.H, D, false, device, &p.k); rc != SA_OK) return rc;
+  if (int rc = check_rows(V, "V", p.c.B, T, p.c.H, D, false, device, &p.v); rc != SA_OK) return rc;
+  p.counts = counts;
+  p.T = T;
+  p.replace = replace != 0;
+  DeviceGuard guard(device);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const long long items = 1LL * T * (D / 16);
+  const dim3 grid(static_cast<unsigned>(items > 0 ? (items + 255) / 256 : 1), p.c.H, p.c.B);
+  if (D == 128)
+    dtype == SA_DTYPE_FP16 ? sa::kv4_append_kernel<128, SA_DTYPE_FP16><<<grid, 256, 0, s>>>(p)
+                           : sa::kv4_append_kernel<128, SA_DTYPE_BF16><<<grid, 256, 0, s>>>(p);
+  else
+    dtype == SA_DTYPE_FP16 ? sa::kv4_append_kernel<64, SA_DTYPE_FP16><<<grid, 256, 0, s>>>(p)
+                           : sa::kv4_append_kernel<64, SA_DTYPE_BF16><<<grid, 256, 0, s>>>(p);
+  return launched("append");
+}
+
+SA_API int sa_kv4_read(const sa_kv4_cache* c, int first, const sa_rows* K, const sa_rows* V,
+                       int dtype, int T, sa_stream stream) {
+  NvtxRange range_("sa_kv4_read");
+  sa::Kv4ReadParams p;
+  int device;
+  if (int rc = check_cache(c, &p.c, &device); rc != SA_OK) return rc;
+  if (int rc = check_call(dtype, T, kMaxTokens, nullptr, device); rc != SA_OK) return rc;
+  if (first < 0 && first != SA_KV4_LAST)
+    return refuse(SA_ERR_INVALID_ARG, "first must be >= 0 or SA_KV4_LAST");
+  const int D = c->head_dim;
+  if (int rc = check_rows(K, "K", p.c.B, T, p.c.H, D, true, device, &p.k); rc != SA_OK) return rc;
+  if (int rc = check_rows(V, "V", p.c.B, T, p.c.H, D, true, device, &p.v); rc != SA_OK) return rc;
+  if (T == 0) return SA_OK;
+  if (K->data == V->data) return refuse(SA_ERR_INVALID_ARG, "K and V must not be the same");
+  p.first = first;
+  p.T = T;
+  DeviceGuard guard(device);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const dim3 grid(static_cast<unsigned>((1LL * T * (D / 16) + 255) / 256), p.c.H, p.c.B);
+  if (D == 128)
+    dtype == SA_DTYPE_FP16 ? sa::kv4_read_kernel<128, SA_DTYPE_FP16><<<grid, 256, 0, s>>>(p)
+                           : sa::kv4_read_kernel<128, SA_DTYPE_BF16><<<grid, 256, 0, s>>>(p);
+  else
+    dtype == SA_DTYPE_FP16 ? sa::kv4_read_kernel<64, SA_DTYPE_FP16><<<grid, 256, 0, s>>>(p)
+                           : sa::kv4_read_kernel<64, SA_DTYPE_BF16><<<grid, 256, 0, s>>>(p);
+  return launched("read");
+}
+
+SA_API size_t sa_kv4_attend_bytes(const sa_kv4_cache* c, int heads, int T, int add_weight) {
+  (void)add_weight;
+  if (check_sizes(c) != SA_OK || T < 0 || T > kMaxTokens || check_heads(c, heads, T) != SA_OK)
+    return 0;
+  return attend_bytes(c, heads, T);
+}
+
+SA_API int sa_kv4_attend(const sa_kv4_cache* c, const sa_rows* Q, const sa_rows* O, int dtype,
+                         int heads, int T, const int32_t* counts, int causal, float scale,
+                         float* lse, int add_weight, void* workspace, size_t workspace_bytes,
+                         sa_stream stream) {
+  NvtxRange range_("sa_kv4_attend");
+  sa::Kv4AttendParams p;
+  int device;
+  if (int rc = check_cache(c, &p.c, &device); rc != SA_OK) return rc;
+  if (int rc = check_call(dtype, T, kMaxTokens, counts, device); rc != SA_OK) return rc;
+  if (int rc = check_heads(c, heads, T); rc != SA_OK) return rc;
+  const int D = c->head_dim;
+  if (int rc = check_rows(Q, "Q", p.c.B, T, heads, D, false, device, &p.q); rc != SA_OK) return rc;
+  if (int rc = check_rows(O, "O", p.c.B, T, heads, D, true, device, &p.o); rc != SA_OK) return rc;
+  if (O->data == Q->data) return refuse(SA_ERR_INVALID_ARG, "O must not alias Q");
+  if (!std::isfinite(scale)) return refuse(SA_ERR_INVALID_ARG, "scale must be finite");
+  std::string why;
+  if (reinterpret_cast<uintptr_t>(lse) & 3u)
+    return refuse(SA_ERR_INVALID_ARG, "lse must be 4-byte aligned");
+  if (!device_memory(lse, device, "lse", &why)) return refuse(SA_ERR_INVALID_ARG, why);
+  if (int rc = check_workspace(workspace, workspace_bytes, attend_bytes(c, heads, T), device);
+      rc != SA_OK)
+    return rc;
+  if (T == 0) return SA_OK;
+  p.counts = counts;
+  p.lse = lse;
+  p.heads = heads;
+  p.group = heads / p.c.H;
+  p.T = T;
+  p.causal = causal != 0;
+  p.scale_log2 = (scale > 0.f ? scale : 1.f / std::sqrt(static_cast<float>(D))) * 1.44269504f;
+  p.lse2 = static_cast<float*>(workspace);
+  DeviceGuard guard(device);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const dim3 grid((T + 3) / 4, heads, p.c.B), wgrid(p.c.N / 128, p.c.H, p.c.B);
+  auto run = [&](auto attend, auto weights) {
+    attend<<<grid, 128, 0, s>>>(p);
+    if (add_weight) weights<<<wgrid, 128, 0, s>>>(p);
+  };
+  if (D == 128)
+    dtype == SA_DTYPE_FP16 ? run(sa::kv4_attend_rows_kernel<128, SA_DTYPE_FP16>,
+                                 sa::kv4_weight_rows_kernel<128, SA_DTYPE_FP16>)
+                           : run(sa::kv4_attend_rows_kernel<128, SA_DTYPE_BF16>,
+                                 sa::kv4_weight_rows_kernel<128, SA_DTYPE_BF16>);
+  else
+    dtype == SA_DTYPE_FP16 ? run(sa::kv4_attend_rows_kernel<64, SA_DTYPE_FP16>,
+                                 sa::kv4_weight_rows_kernel<64, SA_DTYPE_FP16>)
+                           : run(sa::kv4_attend_rows_kernel<64, SA_DTYPE_BF16>,
+                                 sa::kv4_weight_rows_kernel<64, SA_DTYPE_BF16>);
+  return launched("attention");
+}
+
+SA_API size_t sa_kv4_evict_bytes(const sa_kv4_cache* c) {
+  return check_sizes(c) == SA_OK ? evict_bytes(c) : 0;
+}
+
+SA_API int sa_kv4_evict(const sa_kv4_cache* c, int keep, int first, int recent, void* workspace,
+                        size_t workspace_bytes, sa_stream stream) {
+  NvtxRange range_("sa_kv4_evict");
+  sa::Kv4EvictParams p;
+  int device;
+  if (int rc = check_cache(c, &p.c, &device); rc != SA_OK) return rc;
+  if (keep < 1 || first < 0 || recent < 0 || 1LL * first + recent > keep)
+    return refuse(SA_ERR_INVALID_ARG, "need keep >= 1, first, recent >= 0, first + recent <= keep");
+  if (int rc = check_workspace(workspace, workspace_bytes, evict_bytes(c), device); rc != SA_OK)
+    return rc;
+  if (keep >= p.c.N) return SA_OK;  // nothing can be above it
+  p.keep = keep;
+  p.first = first;
+  p.recent = recent;
+  p.n_moves = static_cast<int32_t*>(workspace);
+  p.lists = reinterpret_cast<int32_t*>(
+      static_cast<uint8_t*>(workspace) +
+      align_up(static_cast<size_t>(p.c.B) * p.c.H * sizeof(int32_t), 256));
+  DeviceGuard guard(device);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  sa::kv4_evict_select_kernel<<<dim3(p.c.H, p.c.B), 1024, 0, s>>>(p);
+  const int most = std::min(keep, p.c.N - keep);  // rows that can move, a head
+  const dim3 grid(std::min((most + 15) / 16, 512), p.c.H, p.c.B);
+  if (c->head_dim == 128)
+    sa::kv4_evict_move_kernel<128><<<grid, 256, 0, s>>>(p);
+  else
+    sa::kv4_evict_move_kernel<64><<<grid, 256, 0, s>>>(p);
+  return launched("eviction");
+}
+
+SA_API int sa_kv4_get_status(const sa_kv4_cache* c, sa_stream stream) {
+  Kv4 k;
+  int device;
+  if (int rc = check_cache(c, &k, &device); rc != SA_OK) return rc;
+  DeviceGuard guard(device);
+  unsigned word = 0;
+  cudaError_t e = cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream));
+  if (e == cudaSuccess) e = cudaMemcpy(&word, k.status, sizeof(word), cudaMemcpyDeviceToHost);
+  if (e != cudaSuccess)
+    return refuse(SA_ERR_CUDA, std::string("status: ") + cudaGetErrorString(e));
+  if (word & sa::kDevErrTimeout) return SA_ERR_TIMEOUT;
+  if (word & sa::kDevErrFull) return SA_ERR_FULL;
+  if (word & sa::kDevErrOrder) return SA_ERR_STATE;
+  if (word & sa::kDevWarnSaturated) return SA_ERR_RANGE;
+  return SA_OK;
+}
+
+}  // extern "C"

@@ -16,8 +16,7 @@
 #include <string>
 #include <vector>
 
-#include <nvtx3/nvToolsExt.h>
-
+#include "host_common.h"
 #include "sa_internal.h"
 #include "kernels/attend_simt.cuh"
 #include "kernels/attend_tc.cuh"
@@ -25,23 +24,42 @@
 #include "kernels/exchange.cuh"
 #include "kernels/rope.cuh"
 
+using sa::aligned16;
+using sa::device_memory;
+using sa::g_error;
+using sa::NvtxRange;
 using sa::AttendGroup;
 using sa::AttendParams;
 using sa::AppendParams;
 using sa::RopeTables;
 
-namespace {
+namespace sa {
 
 thread_local std::string g_error;
 
-// NVTX range over one entry point (visible in Nsight timelines; a no-op
-// without a tool attached).
-struct NvtxRange {
-  explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
-  ~NvtxRange() { nvtxRangePop(); }
-  NvtxRange(const NvtxRange&) = delete;
-  NvtxRange& operator=(const NvtxRange&) = delete;
-};
+bool device_memory(const void* p, int device, const char* what, std::string* why) {
+  if (p == nullptr) return true;
+  cudaPointerAttributes a;
+  if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
+    cudaGetLastError();  // clear the sticky-free error of the failed query
+    *why = std::string(what) + " is not a CUDA pointer";
+    return false;
+  }
+  if (a.type == cudaMemoryTypeManaged) return true;
+  if (a.type != cudaMemoryTypeDevice) {
+    *why = std::string(what) + " is host memory; it must be device memory";
+    return false;
+  }
+  if (device >= 0 && a.device != device) {
+    *why = std::string(what) + " is on another device than the handle";
+    return false;
+  }
+  return true;
+}
+
+}  // namespace sa
+
+namespace {
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
@@ -221,32 +239,6 @@ bool encode_blhd(CUtensorMap* map, const void* base, const Derived& d, int rows)
                            static_cast<cuuint64_t>(rows) * d.H * d.D * 2};
   cuuint32_t box[4] = {64, 1, 128, 1};
   return encode_map(map, base, 4, dims, strides, box);
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// Memory type of a tensor pointer, queried on the host before anything is
-// launched: device memory (of `device`, or of any device when device < 0) or
-// managed memory passes; host memory (pageable or pinned) and unknown
-// addresses are refused. NULL passes (presence is checked by the callers).
-bool device_memory(const void* p, int device, const char* what, std::string* why) {
-  if (p == nullptr) return true;
-  cudaPointerAttributes a;
-  if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
-    cudaGetLastError();  // clear the sticky-free error of the failed query
-    *why = std::string(what) + " is not a CUDA pointer";
-    return false;
-  }
-  if (a.type == cudaMemoryTypeManaged) return true;
-  if (a.type != cudaMemoryTypeDevice) {
-    *why = std::string(what) + " is host memory; it must be device memory";
-    return false;
-  }
-  if (device >= 0 && a.device != device) {
-    *why = std::string(what) + " is on another device than the handle";
-    return false;
-  }
-  return true;
 }
 
 // Persistent grid: one CTA per SM at most; with the split tail allowed, a problem
@@ -1564,6 +1556,7 @@ SA_API const char* sa_status_string(int status) {
     case SA_ERR_TIMEOUT: return "SA_ERR_TIMEOUT";
     case SA_ERR_RANGE: return "SA_ERR_RANGE";
     case SA_ERR_BOUNDS: return "SA_ERR_BOUNDS";
+    case SA_ERR_FULL: return "SA_ERR_FULL";
     default: return "SA_ERR_UNKNOWN";
   }
 }

@@ -25,6 +25,10 @@ constexpr int kModeAligned = 2;
 constexpr unsigned kDevErrTimeout = 1u;
 constexpr unsigned kDevWarnSaturated = 2u;
 constexpr unsigned kDevErrBounds = 4u;
+// 4-bit caches: rows beyond the capacity were dropped; a causal attention over
+// rows that an eviction had put out of order.
+constexpr unsigned kDevErrFull = 8u;
+constexpr unsigned kDevErrOrder = 16u;
 
 // Device-side bounds checks of the checked build (libsa_checked.so, compiled
 // with SA_DEVICE_CHECKS): before a kernel reads or writes global memory

@@ -26,7 +26,7 @@
  *  The extensions cite their sections at each call: reference image and chunk
  *  length (sa_set_reference, sa_append_chunk_frames), block sparsity
  *  (sa_attend_sparse), frame-aligned editing (sa_attend_aligned), Ulysses
- *  exchange (sa_exchange_*).
+ *  exchange (sa_exchange_*), a cache held in 4 bits (sa_kv4_*).
  *
  * Conventions shared by every call
  *  - Tensors are bfloat16, row-major [B, L, H, D] (batch, token of the chunk,
@@ -74,8 +74,10 @@ typedef enum {
   SA_ERR_TIMEOUT = 5,      /* a kernel gave up a bounded wait (device status) */
   SA_ERR_RANGE = 6,        /* an operand left the fp16 range of the score MMA and
                               was saturated (device status; outputs degraded) */
-  SA_ERR_BOUNDS = 7        /* checked build only: a kernel skipped an access past
+  SA_ERR_BOUNDS = 7,       /* checked build only: a kernel skipped an access past
                               the end of a buffer (a library bug; device status) */
+  SA_ERR_FULL = 8          /* rows appended to a 4-bit cache did not fit its capacity
+                              and were dropped (device status) */
 } sa_status;
 
 typedef enum { SA_TIER_NOISY = 0, SA_TIER_CLEAN = 1 } sa_tier;
@@ -416,6 +418,127 @@ SA_API int sa_ipc_free(void* dev_ptr);
 SA_API int sa_ipc_handle(const void* dev_ptr, void* handle_out);
 SA_API int sa_ipc_open(const void* handle, void** dev_ptr_out);
 SA_API int sa_ipc_close(void* dev_ptr);
+
+/* ---- A KV cache held in 4 bits, its attention, and eviction by accumulated
+ * attention weight. A second kind of cache next to the handle's chunk slots
+ * ("Vidu S2 vs PixVerse R2：实时视频的两条技术路线", section 选择三：有上限的记忆: a bounded
+ * memory): rows (tokens) instead of chunks, 4.5 bits a value instead of 16, any
+ * number of query heads per KV head, sequences of different lengths, and the
+ * rows that drew least attention evicted instead of the oldest. It serves one
+ * generated token at a time as well as whole chunks.
+ *
+ * Every buffer is the caller's; these calls keep nothing. Rows are stored as
+ * they are passed: position encoding is applied by the caller, to K before
+ * sa_kv4_append and to Q before sa_kv4_attend, so a row stays valid while rows
+ * around it are evicted. Numbers of rows live on the device (seq), so captured
+ * calls can be replayed as the sequences grow.
+ *
+ * Format: 16 consecutive values of a row's D share a scale. scale = the smallest
+ * value of the scale format >= max|x| / 6, at most 10240; code = x / scale
+ * rounded to e2m1 (nearest, ties to even): magnitudes 0 .5 1 1.5 2 3 4 6, bit 3
+ * the sign. Values 2i and 2i + 1 are the low and the high half of byte i. A scale
+ * is one byte b, the value of the fp16 with bits b << 7 (five exponent bits,
+ * three fraction bits, no sign); b <= 226. A stored value is code * scale: six
+ * significant bits, so exact in fp16 and bf16. Values beyond +-61440 are stored
+ * as +-61440 and values that are not finite as some finite value; both set
+ * SA_ERR_RANGE in the status word. */
+#define SA_DTYPE_BF16 0
+#define SA_DTYPE_FP16 1
+
+/* A 4-bit cache: sizes and device buffers, contiguous, 16-byte aligned, on one
+ * device. A capacity must be a multiple of 128. The status word and seq must be
+ * zero at first (sa_kv4_reset); the other buffers need no initial values. */
+typedef struct {
+  int32_t batch;      /* B >= 1 sequences */
+  int32_t kv_heads;   /* Hk >= 1 */
+  int32_t head_dim;   /* D: 64 or 128 */
+  int32_t capacity;   /* N: rows each sequence can hold, a multiple of 128 */
+  uint8_t* k_codes;   /* [B, Hk, N, D / 2] */
+  uint8_t* v_codes;   /* [B, Hk, N, D / 2] */
+  uint8_t* k_scales;  /* [B, Hk, N, D / 16] */
+  uint8_t* v_scales;  /* [B, Hk, N, D / 16] */
+  int32_t* pos;       /* [B, Hk, N]: place of the row in its sequence, counted from
+                         0 over all rows ever appended */
+  float* weight;      /* [B, Hk, N]: attention weight the row has drawn */
+  int32_t* seq;       /* [4, B]: rows held; rows appended in all; rows of the last
+                         append (0 after an eviction); rows appended since the last
+                         eviction */
+  uint32_t* status;   /* [4]: status word, then the library's counters */
+} sa_kv4_cache;
+
+/* Rows of [B, T, heads, D] in device memory: value (b, t, h, d) is element
+ * b * stride_b + t * stride_t + h * stride_h + d of data (16-byte aligned, strides
+ * multiples of 8 and >= 0), so a slice of a fused projection can be passed. */
+typedef struct {
+  void* data;
+  int64_t stride_b, stride_t, stride_h;
+} sa_rows;
+
+/* Empty the cache: seq and status to zero, asynchronously on `stream`. */
+SA_API int sa_kv4_reset(const sa_kv4_cache* c, sa_stream stream);
+
+/* Quantise T new rows of K and V ([B, T, Hk, D], dtype SA_DTYPE_*) and put them
+ * behind the rows held; their weight is 0. counts: device int32 [B], sequence b
+ * gets its first counts[b] rows (clamped to 0..T), or NULL for T each. replace != 0
+ * first drops the rows of the last append (a chunk's next denoising step, draft
+ * tokens that were refused); after an eviction there are none to drop. Rows
+ * beyond the capacity are dropped and set SA_ERR_FULL. T = 0 is allowed. One
+ * launch. Calls on one cache must be ordered on the GPU. */
+SA_API int sa_kv4_append(const sa_kv4_cache* c, const sa_rows* K, const sa_rows* V, int dtype,
+                         int T, const int32_t* counts, int replace, sa_stream stream);
+
+/* Write the stored values of rows first .. first + T - 1 of each sequence to K and
+ * V ([B, T, Hk, D], overlapping neither each other nor the cache), or with
+ * first = SA_KV4_LAST the rows of the last append. Rows not held are left as they
+ * were. */
+#define SA_KV4_LAST (-1)
+SA_API int sa_kv4_read(const sa_kv4_cache* c, int first, const sa_rows* K, const sa_rows* V,
+                       int dtype, int T, sa_stream stream);
+
+/* Attention of T query tokens per sequence over the rows held:
+ *   O = softmax(scale Q K^T) V
+ * Q, O: [B, T, heads, D], dtype SA_DTYPE_*; heads is a multiple of Hk, and query
+ * head h reads KV head h / (heads / Hk). counts: device int32 [B], sequence b has
+ * counts[b] query tokens (clamped to 0..T), or NULL for T each; O and lse of the
+ * tokens behind them are left as they were. causal == 0: every query reads every
+ * row held. causal != 0: the queries are those of the last rows appended, query t
+ * of counts[b] reading the rows up to row held - counts[b] + t. That needs
+ * counts[b] <= the rows appended since the last eviction unless counts[b] <= 1,
+ * else SA_ERR_STATE is set in the status word (rows are no longer in order; the
+ * result is unspecified). scale <= 0 selects 1/sqrt(D). lse: [B, heads, T] fp32,
+ * natural log of the sum of exp of the scaled scores, or NULL; with it the result
+ * merges with an attention over other keys. A query that sees no row gets O = 0,
+ * lse = -inf.
+ * add_weight != 0 adds to weight[b, k, j], for every row j, the sum of the softmax
+ * probabilities that the sequence's queries of KV head k's group gave it.
+ * Scores, softmax statistics and sums are fp32; Q enters the products as fp16
+ * after a scaling of its row by a power of two, P as fp16, K and V exactly.
+ * Workspace: sa_kv4_attend_bytes(...) bytes of device memory, 256-byte aligned,
+ * contents free before and after; calls that share it must be ordered. Results do
+ * not depend on timing: repeated calls give the same bits. */
+SA_API size_t sa_kv4_attend_bytes(const sa_kv4_cache* c, int heads, int T, int add_weight);
+SA_API int sa_kv4_attend(const sa_kv4_cache* c, const sa_rows* Q, const sa_rows* O, int dtype,
+                         int heads, int T, const int32_t* counts, int causal, float scale,
+                         float* lse, int add_weight, void* workspace, size_t workspace_bytes,
+                         sa_stream stream);
+
+/* Evict rows until every sequence holds at most `keep`. Each KV head decides for
+ * itself: rows with pos < first or pos >= rows appended in all - recent stay
+ * (first + recent <= keep); of the others the rows of the largest weight stay, of
+ * equal weights the lower row, a weight that is NaN counting below every number.
+ * Rows kept beyond row keep - 1 move into the places of the evicted ones below it,
+ * the j-th of the former to the j-th of the latter, with code, scale, pos and
+ * weight; all other rows stay where they are. Order among rows is lost (see
+ * causal above). A sequence of at most keep rows is left as it is. Workspace as
+ * above, sa_kv4_evict_bytes(c) bytes. */
+SA_API size_t sa_kv4_evict_bytes(const sa_kv4_cache* c);
+SA_API int sa_kv4_evict(const sa_kv4_cache* c, int keep, int first, int recent, void* workspace,
+                        size_t workspace_bytes, sa_stream stream);
+
+/* Wait for `stream`, then read the cache's status word: SA_OK, SA_ERR_TIMEOUT,
+ * SA_ERR_FULL, SA_ERR_STATE or SA_ERR_RANGE (the first that applies since the last
+ * sa_kv4_reset). The text of a refused call is sa_last_error(NULL). */
+SA_API int sa_kv4_get_status(const sa_kv4_cache* c, sa_stream stream);
 
 /* Slot of chunk id `chunk` in a tier (-1 if it is never stored). Host only. */
 SA_API int sa_slot_of(const sa_config* cfg, int32_t chunk);
