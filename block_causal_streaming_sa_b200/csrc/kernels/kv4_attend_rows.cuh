@@ -2,25 +2,9 @@
 // for every size. Scores take a key row per lane, outputs D / 32 values per lane.
 #pragma once
 
-#include "kv4_format.cuh"
-#include "ptx.cuh"
+#include "kv4_params.cuh"
 
 namespace sa {
-
-struct Kv4AttendParams {
-  Kv4 c;
-  Kv4Rows q, o;
-  const int32_t* counts;
-  float* lse;  // [B][heads][T] or null
-  int heads, group, T, causal;
-  float scale_log2;
-  float* lse2;  // workspace [B][heads][T]: base-2 log-sum-exp of every query
-};
-
-// Rows that query t of sequence b reads.
-__device__ __forceinline__ int rows_seen(const Kv4AttendParams& p, int held, int n_tok, int t) {
-  return p.causal ? max(min(held - n_tok + t + 1, held), 0) : held;
-}
 
 template <int D, int kDtype>
 __global__ void __launch_bounds__(128) kv4_attend_rows_kernel(
@@ -102,7 +86,7 @@ __global__ void __launch_bounds__(128) kv4_attend_rows_kernel(
     const size_t at = (static_cast<size_t>(b) * p.heads + hq) * p.T + t;
     const float l2 = l > 0.f ? m + log2f(l) : -INFINITY;
     if (p.lse != nullptr) p.lse[at] = l2 * 0.69314718055994531f;
-    p.lse2[at] = l2;
+    p.scores[at] = l2;
   }
 }
 
@@ -148,7 +132,7 @@ __global__ void __launch_bounds__(128) kv4_weight_rows_kernel(
         s = fmaf(v.x, k[d], s);
         s = fmaf(v.y, k[d + 1], s);
       }
-      const float l2 = p.lse2[(static_cast<size_t>(b) * p.heads + hq) * p.T + t];
+      const float l2 = p.scores[(static_cast<size_t>(b) * p.heads + hq) * p.T + t];
       sum += exp2f(s * p.scale_log2 - l2);
     }
   }

@@ -1,0 +1,691 @@
+// Attention of few query rows over a 4-bit cache: one generated token, some drafts.
+//
+// Bound by reading the cache: D + D / 8 bytes a row and KV head. What a row costs on
+// an SM apart from that is its dequantisation, so the products go to the register
+// matrix instruction (mma m16n8k16): its operands come from shared memory straight
+// into the registers the codes are unpacked in, while tcgen05 operands would have to
+// be written back to shared memory at 16 bits and read again (1 KB a row and head
+// against 288 bytes), more than the shared memory of an SM carries at HBM speed;
+// the tensor core itself is idle either way (8 useful query rows of the tile).
+//
+//  * S^T = K Q^T: 16 cache rows x 8 query rows x 16 values. The order of the values
+//    along D is free as long as both operands agree, so a lane's K registers are the
+//    codes of one aligned 16-byte (D = 64: 8-byte) piece of a row, in order.
+//  * O^T = V^T P^T: 16 values x 8 query rows x 16 cache rows. A lane owns D / 8
+//    consecutive values of four rows; two rows' codes are interleaved by byte
+//    permutes after the conversion. P^T comes from S^T by transposing 8 x 8 blocks
+//    (movmatrix); both keep query rows on the same lanes, so the softmax statistics
+//    never move.
+//  * The running maximum of a query row is raised only when a score exceeds it by
+//    more than 2^8 (checked by one vote a tile): no reduction across lanes otherwise.
+//    P stays below 2^8 and l and O are fp32.
+//  * Each warp streams tiles of 32 rows through a ring of its own (bulk copies by
+//    its lane 0, an mbarrier a stage), so warps never wait for one another.
+//  * The rows of all sequences and heads are one line of tiles, cut into equal
+//    ranges, one a block, whatever the lengths: long rows are split over blocks and
+//    short ones share one. A range that crosses heads leaves one partial result per
+//    head; (block + head) numbers them without gaps growing beyond blocks + heads.
+//    kv4_join_kernel merges them in that order.
+#pragma once
+
+#include "kv4_params.cuh"
+
+namespace sa {
+
+template <int D, int NT>
+struct DecodeShape {
+  static constexpr int kWarps = 4;
+  static constexpr int kRows = 8 * NT;  // query rows of a block
+  static constexpr int kTile = 32;      // cache rows of a warp's tile
+  static constexpr int kCodes = kTile * D / 2, kScales = kTile * D / 16;
+  static constexpr int kStageBytes = 2 * (kCodes + kScales);
+  static constexpr int kStages = D == 128 ? 3 : 4;  // 55 KB (D 128): four blocks an SM
+  static constexpr int kRing = kWarps * kStages * kStageBytes;
+  static constexpr int kMergeStride = D + 4;
+  static constexpr int kMerge = kWarps * kRows * kMergeStride * 4;
+  static constexpr int kData = kRing > kMerge ? kRing : kMerge;
+  static constexpr int kOffMl = kData;                             // float2 [warp][row]
+  static constexpr int kOffQ = kOffMl + kWarps * kRows * 8;        // fragments, NT > 1
+  static constexpr int kOffSl = kOffQ + (NT > 1 ? kRows * D * 2 : 0);
+  static constexpr int kOffBar = kOffSl + kRows * 4;
+  static constexpr int kSmem = kOffBar + kWarps * kStages * 8 + 16;
+  static constexpr int kBlocksPerSm = NT == 1 ? 4 : NT == 2 ? 3 : 2;
+};
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=h"(v) : "r"(a));
+  return v;
+}
+
+// Cache row, within 16, of row r of the matrix tiles: an order in which neither the
+// K loads (lanes of equal r / 4: neighbours in r) nor the V loads (every second r)
+// meet the same banks more often than their bytes make necessary.
+template <int D>
+__device__ __forceinline__ int tile_row(int r) {
+  if constexpr (D == 128) return r ^ ((r >> 1) & 1);
+  constexpr unsigned order = 0x57463120u;  // 0 2 1 3 6 4 7 5
+  return (r & 8) | static_cast<int>((order >> ((r & 7) * 4)) & 7u);
+}
+
+// Where the tiles of all (sequence, head, row block) units lie on the line. Every
+// block derives it from the lengths; lanes take a sequence each.
+struct Line {
+  int share;        // tiles of a block
+  long long total;  // tiles in all
+};
+
+__device__ __forceinline__ int unit_tiles(const Kv4AttendParams& p, int b, int tile) {
+  if (tokens_of(p.counts, b, p.T) == 0) return 0;
+  return (rows_held(p.c, b) + tile - 1) / tile;
+}
+
+// Tiles of the sequences before `upto`, by a whole warp.
+__device__ __forceinline__ long long tiles_before(const Kv4AttendParams& p, int upto, int tile,
+                                                  int lane) {
+  long long sum = 0;
+  for (int b = lane; b < upto; b += 32) sum += unit_tiles(p, b, tile);
+#pragma unroll
+  for (int k = 16; k; k >>= 1) sum += __shfl_xor_sync(~0u, sum, k);
+  return sum * p.c.H * p.row_blocks;
+}
+
+// At least 4 tiles a block, so that every warp has one.
+__device__ __forceinline__ Line line_of(const Kv4AttendParams& p, int blocks, int tile, int lane) {
+  Line l;
+  l.total = tiles_before(p, p.c.B, tile, lane);
+  l.share = static_cast<int>(max((l.total + blocks - 1) / blocks, 4LL));
+  return l;
+}
+
+template <int D, int NT, int kDtype, bool kScores>
+__global__ void __launch_bounds__(128, DecodeShape<D, NT>::kBlocksPerSm)
+    kv4_decode_kernel(const __grid_constant__ Kv4AttendParams p) {
+  using S = DecodeShape<D, NT>;
+  constexpr int KS = D / 16;       // steps along D of S^T = tiles of values of O^T
+  constexpr int KW = D / 32;       // words of K codes of a lane and row
+  constexpr int VW = D / 64;       // words of V codes of a lane and row
+  extern __shared__ __align__(128) uint8_t smem[];
+  const Kv4& c = p.c;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, tig = lane & 3;
+  const uint32_t sbase = ptx::smem_addr(smem);
+  const uint32_t ring = sbase + warp * S::kStages * S::kStageBytes;
+  const uint32_t bars = sbase + S::kOffBar + warp * S::kStages * 8;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kSmem - 16);
+  if (threadIdx.x == 0) *abort_flag = 0;
+  if (lane == 0) {
+    for (int s = 0; s < S::kStages; ++s) ptx::mbar_init(bars + 8 * s, 1);
+    ptx::fence_mbar_init();
+  }
+  __syncthreads();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  const Line line = line_of(p, gridDim.x, S::kTile, lane);
+  long long at = static_cast<long long>(blockIdx.x) * line.share;
+  const long long stop = min(at + line.share, line.total);
+  if (blockIdx.x == 0)
+    for (int b = threadIdx.x; b < c.B; b += 128) check_order(p, b, tokens_of(p.counts, b, p.T));
+  if (at >= stop) return;
+
+  // the sequence that holds tile `at`
+  int b = 0;
+  long long b0 = 0;  // first tile of sequence b
+  while (true) {
+    const long long n = 1LL * unit_tiles(p, b, S::kTile) * c.H * p.row_blocks;
+    if (at < b0 + n) break;
+    b0 += n;
+    ++b;
+  }
+  unsigned loads = 0, uses = 0;  // stages filled and emptied so far by this warp
+  bool ok = true;
+
+  while (at < stop) {
+    // one unit: rows [t0, t1) tiles of sequence b, KV head h, query rows row0 ..
+    const int per_unit = unit_tiles(p, b, S::kTile);
+    if (per_unit == 0 || at >= b0 + 1LL * per_unit * c.H * p.row_blocks) {
+      b0 += 1LL * per_unit * c.H * p.row_blocks;
+      ++b;
+      continue;
+    }
+    const int unit_in_b = static_cast<int>((at - b0) / per_unit);
+    const int t0 = static_cast<int>((at - b0) % per_unit);
+    const int t1 = static_cast<int>(min(static_cast<long long>(per_unit), t0 + (stop - at)));
+    const int h = unit_in_b / p.row_blocks, rb = unit_in_b % p.row_blocks;
+    const int unit = b * c.H * p.row_blocks + unit_in_b;
+    const int held = rows_held(c, b), n_tok = tokens_of(p.counts, b, p.T);
+    const int n_rows = n_tok * p.group, row0 = rb * S::kRows;
+    const size_t plane = (static_cast<size_t>(b) * c.H + h) * c.N;
+
+    auto fill = [&](int tile) {  // lane 0
+      const unsigned s = loads % S::kStages;
+      const uint32_t dst = ring + s * S::kStageBytes, bar = bars + 8 * s;
+      const size_t row = plane + static_cast<size_t>(tile) * S::kTile;
+      ptx::mbar_arrive_expect_tx(bar, S::kStageBytes);
+      bulk_load(dst, c.k_codes + row * (D / 2), S::kCodes, bar);
+      bulk_load(dst + S::kCodes, c.v_codes + row * (D / 2), S::kCodes, bar);
+      bulk_load(dst + 2 * S::kCodes, c.k_scales + row * (D / 16), S::kScales, bar);
+      bulk_load(dst + 2 * S::kCodes + S::kScales, c.v_scales + row * (D / 16), S::kScales, bar);
+    };
+    int next = t0 + warp;  // next tile to load
+    for (int s = 0; ok && s < S::kStages && next < t1; ++s, next += S::kWarps, ++loads)
+      if (lane == 0) fill(next);
+
+    // Query fragments: lane (g, tig) of step k holds values 4 k .. 4 k + 3 of its
+    // D / 4 consecutive ones of query row g. Scaled to fp16 by a power of two a row.
+    uint32_t qf[NT == 1 ? KS : 1][2];
+    float sl[NT][2];  // scale * log2 e / row factor of this lane's query columns
+    float* s_sl = reinterpret_cast<float*>(smem + S::kOffSl);
+    if constexpr (NT > 1) __syncthreads();  // the previous unit is done with them
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      if (NT > 1 && nt % S::kWarps != warp) continue;
+      const int r = row0 + nt * 8 + g;
+      float2 v[D / 8];
+      float amax = 0.f;
+      if (r < n_rows) {
+        const uint16_t* src = static_cast<const uint16_t*>(p.q.data) + b * p.q.sb +
+                              (r / p.group) * p.q.st + (h * p.group + r % p.group) * p.q.sh +
+                              tig * (D / 4);
+        uint4 w[D / 32];
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(src) + i);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          v[4 * i] = unpack2<kDtype>(w[i].x);
+          v[4 * i + 1] = unpack2<kDtype>(w[i].y);
+          v[4 * i + 2] = unpack2<kDtype>(w[i].z);
+          v[4 * i + 3] = unpack2<kDtype>(w[i].w);
+        }
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) amax = fmaxf(amax, fmaxf(fabsf(v[i].x), fabsf(v[i].y)));
+      } else {
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) v[i] = make_float2(0.f, 0.f);
+      }
+      amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 2));
+      const float f = row_factor(amax);
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        const uint32_t x = pack2<SA_DTYPE_FP16>(v[2 * k].x * f, v[2 * k].y * f);
+        const uint32_t y = pack2<SA_DTYPE_FP16>(v[2 * k + 1].x * f, v[2 * k + 1].y * f);
+        if constexpr (NT == 1) {
+          qf[k][0] = x;
+          qf[k][1] = y;
+        } else {
+          *reinterpret_cast<uint2*>(smem + S::kOffQ + ((k * NT + nt) * 32 + lane) * 8) =
+              make_uint2(x, y);
+        }
+      }
+      const float scale = p.scale_log2 / f;
+      if constexpr (NT == 1) {  // lane 4 n (or any of its four) holds row n's
+        sl[0][0] = __shfl_sync(~0u, scale, 8 * tig);
+        sl[0][1] = __shfl_sync(~0u, scale, 8 * tig + 4);
+      } else {
+        if (tig == 0) s_sl[nt * 8 + g] = scale;
+      }
+    }
+    if constexpr (NT > 1) {
+      __syncthreads();
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        sl[nt][0] = s_sl[nt * 8 + 2 * tig];
+        sl[nt][1] = s_sl[nt * 8 + 2 * tig + 1];
+      }
+    }
+
+    float o[KS][NT][4], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[k][nt][i] = 0.f;
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+    }
+    // rows before this see no mask
+    const int open = p.causal ? max(held - n_tok + 1, 0) : held;
+
+    for (int t = t0 + warp; ok && t < t1; t += S::kWarps) {
+      const unsigned st = uses % S::kStages;
+      ok = ptx::mbar_wait(bars + 8 * st, (uses / S::kStages) & 1, abort_flag, c.status);
+      if (!ok) break;
+      ++uses;
+      const uint32_t kc = ring + st * S::kStageBytes, vc = kc + S::kCodes;
+      const uint32_t ksc = vc + S::kCodes, vsc = ksc + S::kScales;
+      const int j0 = t * S::kTile;
+      const bool edge = j0 + S::kTile > open;
+
+      // ---- S^T
+      float s[2][NT][4];
+      uint32_t kw[2][2][KW], ksb[2][2];
+#pragma unroll
+      for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+        for (int hi = 0; hi < 2; ++hi) {
+          const int row = sub * 16 + tile_row<D>(g + 8 * hi);
+          if constexpr (D == 128) {
+            const uint4 w = lds128(kc + row * 64 + tig * 16);
+            kw[sub][hi][0] = w.x;
+            kw[sub][hi][1] = w.y;
+            kw[sub][hi][KW - 2] = w.z;
+            kw[sub][hi][KW - 1] = w.w;
+            ksb[sub][hi] = lds16(ksc + row * 8 + tig * 2);
+          } else {
+            const uint2 w = lds64(kc + row * 32 + tig * 8);
+            kw[sub][hi][0] = w.x;
+            kw[sub][hi][KW - 1] = w.y;
+            ksb[sub][hi] = lds8(ksc + row * 4 + tig);
+          }
+        }
+#pragma unroll
+      for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[sub][nt][i] = 0.f;
+#pragma unroll
+      for (int w = 0; w < KW; ++w) {  // a word is two steps
+        uint32_t a[2][2][4];
+#pragma unroll
+        for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+          for (int hi = 0; hi < 2; ++hi) {
+            codes_to_f16(kw[sub][hi][w], a[sub][hi]);
+            const uint32_t sc = scale_f16x2(D == 128 ? (ksb[sub][hi] >> (8 * (w >> 1))) & 255u
+                                                     : ksb[sub][hi]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a[sub][hi][i] = mul_f16x2(a[sub][hi][i], sc);
+          }
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const int k = 2 * w + half;
+            uint32_t b0, b1;
+            if constexpr (NT == 1) {
+              b0 = qf[k][0];
+              b1 = qf[k][1];
+            } else {
+              const uint2 f = lds64(sbase + S::kOffQ + ((k * NT + nt) * 32 + lane) * 8);
+              b0 = f.x;
+              b1 = f.y;
+            }
+#pragma unroll
+            for (int sub = 0; sub < 2; ++sub)
+              mma_16816(s[sub][nt], a[sub][0][2 * half], a[sub][1][2 * half],
+                        a[sub][0][2 * half + 1], a[sub][1][2 * half + 1], b0, b1);
+          }
+      }
+
+      // ---- softmax: s[sub][nt] = rows g, g, g + 8, g + 8; queries 2 tig, 2 tig + 1, ..
+      bool raise = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[sub][nt][i] *= sl[nt][i & 1];
+        if (edge) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = row0 + nt * 8 + 2 * tig + (i & 1);
+            const int end = rows_seen(p, held, n_tok, r / p.group);
+#pragma unroll
+            for (int sub = 0; sub < 2; ++sub)
+              if (j0 + sub * 16 + tile_row<D>(g + (i & 2) * 4) >= end)
+                s[sub][nt][i] = -INFINITY;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          raise |= fmaxf(fmaxf(s[0][nt][i], s[0][nt][i + 2]), fmaxf(s[1][nt][i], s[1][nt][i + 2])) >
+                   m[nt][i] + 8.f;
+      }
+      if (__any_sync(~0u, raise)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float mx = fmaxf(fmaxf(s[0][nt][i], s[0][nt][i + 2]),
+                             fmaxf(s[1][nt][i], s[1][nt][i + 2]));
+#pragma unroll
+            for (int k = 4; k < 32; k <<= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, k));
+            mx = fmaxf(mx, m[nt][i]);
+            const float a = mx > m[nt][i] ? ptx::ex2(m[nt][i] - mx) : 1.f;
+            m[nt][i] = mx;
+            l[nt][i] *= a;
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+              o[k][nt][i] *= a;
+              o[k][nt][i + 2] *= a;
+            }
+          }
+      }
+      uint32_t pb[2][NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float n0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
+        const float n1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+#pragma unroll
+        for (int sub = 0; sub < 2; ++sub) {
+          if constexpr (kScores) {
+            const int r = row0 + nt * 8 + 2 * tig;
+            if (r < p.score_rows)
+#pragma unroll
+              for (int hi = 0; hi < 2; ++hi) {
+                const size_t row = plane + j0 + sub * 16 + tile_row<D>(g + 8 * hi);
+                *reinterpret_cast<float2*>(p.scores + row * p.score_rows + r) =
+                    make_float2(s[sub][nt][2 * hi], s[sub][nt][2 * hi + 1]);
+              }
+          }
+          const float p0 = ptx::ex2(s[sub][nt][0] - n0), p1 = ptx::ex2(s[sub][nt][1] - n1);
+          const float p2 = ptx::ex2(s[sub][nt][2] - n0), p3 = ptx::ex2(s[sub][nt][3] - n1);
+          l[nt][0] += p0 + p2;
+          l[nt][1] += p1 + p3;
+          pb[sub][nt][0] = transpose_8x8(pack2<SA_DTYPE_FP16>(p0, p1));
+          pb[sub][nt][1] = transpose_8x8(pack2<SA_DTYPE_FP16>(p2, p3));
+        }
+      }
+
+      // ---- O^T: a lane's rows are 2 tig, 2 tig + 1, and those + 8; its values
+      // D / 8 g .. (matrix rows g and g + 8 of tile k are values 2 k and 2 k + 1)
+#pragma unroll
+      for (int sub = 0; sub < 2; ++sub) {
+        uint32_t vw[4][VW], sc[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int row = sub * 16 + tile_row<D>(2 * tig + (e & 1) + 8 * (e >> 1));
+          uint32_t byte;
+          if constexpr (D == 128) {
+            const uint2 w = lds64(vc + row * 64 + g * 8);
+            vw[e][0] = w.x;
+            vw[e][VW - 1] = w.y;
+            byte = lds8(vsc + row * 8 + g);
+          } else {
+            vw[e][0] = lds32(vc + row * 32 + g * 4);
+            byte = lds8(vsc + row * 4 + (g >> 1));
+          }
+          // rows not held may hold any bytes: a scale that is NaN must not meet P = 0
+          if (edge && j0 + row >= held) byte = 0;
+          sc[e] = scale_f16x2(byte);
+        }
+#pragma unroll
+        for (int w = 0; w < VW; ++w) {
+          uint32_t v[4][4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            codes_to_f16(vw[e][w], v[e]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[e][i] = mul_f16x2(v[e][i], sc[e]);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t a0 = __byte_perm(v[0][i], v[1][i], 0x5410);
+            const uint32_t a1 = __byte_perm(v[0][i], v[1][i], 0x7632);
+            const uint32_t a2 = __byte_perm(v[2][i], v[3][i], 0x5410);
+            const uint32_t a3 = __byte_perm(v[2][i], v[3][i], 0x7632);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_16816(o[4 * w + i][nt], a0, a1, a2, a3, pb[sub][nt][0], pb[sub][nt][1]);
+          }
+        }
+      }
+      __syncwarp();  // every lane has read the stage
+      if (next < t1) {
+        if (lane == 0) fill(next);
+        next += S::kWarps;
+        ++loads;
+      }
+    }
+    // (after an abort the blocks' barriers below are still met; the result is void)
+
+    // ---- merge the four warps in shared memory (the rings are empty now)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int k = 4; k < 32; k <<= 1) l[nt][i] += __shfl_xor_sync(~0u, l[nt][i], k);
+    __syncthreads();
+    float2* s_ml = reinterpret_cast<float2*>(smem + S::kOffMl);
+    float* s_o = reinterpret_cast<float*>(smem);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = nt * 8 + 2 * tig + i;
+        if (g == 0) s_ml[warp * S::kRows + r] = make_float2(m[nt][i], l[nt][i]);
+        float* dst = s_o + (warp * S::kRows + r) * S::kMergeStride + g * (D / 8);
+#pragma unroll
+        for (int k = 0; k < KS; k += 2)
+          *reinterpret_cast<float4*>(dst + 2 * k) =
+              make_float4(o[k][nt][i], o[k][nt][i + 2], o[k + 1][nt][i], o[k + 1][nt][i + 2]);
+      }
+    }
+    __syncthreads();
+    const size_t slot = static_cast<size_t>(blockIdx.x) + unit;
+    for (int i = threadIdx.x; i < S::kRows * (D / 4); i += 128) {
+      const int r = i / (D / 4), d = (i % (D / 4)) * 4;
+      if (row0 + r >= n_rows) break;
+      float mx = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < S::kWarps; ++w) mx = fmaxf(mx, s_ml[w * S::kRows + r].x);
+      const float ref = mx == -INFINITY ? 0.f : mx;
+      float sum = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < S::kWarps; ++w) {
+        const float2 ml = s_ml[w * S::kRows + r];
+        const float a = ptx::ex2(ml.x - ref);
+        const float4 x =
+            *reinterpret_cast<float4*>(s_o + (w * S::kRows + r) * S::kMergeStride + d);
+        sum += ml.y * a;
+        acc.x += x.x * a;
+        acc.y += x.y * a;
+        acc.z += x.z * a;
+        acc.w += x.w * a;
+      }
+      *reinterpret_cast<float4*>(p.part_o + (slot * S::kRows + r) * D + d) = acc;
+      if (d == 0) p.part_ml[slot * S::kRows + r] = make_float2(mx, sum);
+    }
+    at += t1 - t0;
+    // the copies of the next unit go through the asynchronous proxy into memory that
+    // was just read and written here
+    __syncthreads();
+    ptx::fence_proxy_async_smem();
+  }
+  // after an abort: copies still under way land before the block's memory goes
+  if (!ok) {
+    volatile int none = 0;
+    for (; uses < loads; ++uses)
+      ptx::mbar_wait(bars + 8 * (uses % S::kStages), (uses / S::kStages) & 1, &none, c.status);
+  }
+}
+
+// Merge of the partial results of kv4_decode_kernel, a warp per query row, and the
+// rows' weights. Blocks below join_blocks merge; the others add weights, `kKeys`
+// cache rows of one (sequence, KV head) each: they derive the log-sum-exp of its
+// query rows from the same partial results, so no order among blocks is needed.
+constexpr int kJoinKeys = 512;
+
+template <int D, int kRows, int kDtype>
+__global__ void __launch_bounds__(128)
+    kv4_join_kernel(const __grid_constant__ Kv4AttendParams p, int blocks, int join_blocks) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Kv4& c = p.c;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool joins = static_cast<int>(blockIdx.x) < join_blocks;
+  // join: block = (unit, four rows of it); weights: block = (head plane, chunk of rows)
+  const int row_groups = kRows / 4;
+  const int chunks = (c.N + kJoinKeys - 1) / kJoinKeys;
+  const int id = joins ? blockIdx.x / row_groups : (blockIdx.x - join_blocks) / chunks;
+  const int units_b = c.H * p.row_blocks;
+  const int b = joins ? id / units_b : id / c.H;
+  const int held = rows_held(c, b), n_tok = tokens_of(p.counts, b, p.T);
+  const int n_rows = n_tok * p.group;
+  if (n_rows == 0) return;
+  const Line line = line_of(p, blocks, 32, lane);
+  const long long b0 = tiles_before(p, b, 32, lane);
+  const int per_unit = unit_tiles(p, b, 32);
+
+  // Partial results of one query row: slots first .. last (none: last < first).
+  auto slots_of = [&](int unit_in_b, size_t& first, size_t& last) {
+    const long long u0 = b0 + 1LL * unit_in_b * per_unit;
+    const size_t unit = static_cast<size_t>(b) * units_b + unit_in_b;
+    if (per_unit == 0) {
+      first = 1;
+      last = 0;
+      return;
+    }
+    first = u0 / line.share + unit;
+    last = (u0 + per_unit - 1) / line.share + unit;
+  };
+  auto statistics = [&](size_t first, size_t last, int r, float& mx, float& sum) {
+    mx = -INFINITY;
+    for (size_t s = first + lane; s <= last; s += 32) mx = fmaxf(mx, p.part_ml[s * kRows + r].x);
+#pragma unroll
+    for (int k = 16; k; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, k));
+    const float ref = mx == -INFINITY ? 0.f : mx;
+    sum = 0.f;
+    for (size_t s = first + lane; s <= last; s += 32) {
+      const float2 ml = p.part_ml[s * kRows + r];
+      sum += ml.y * ptx::ex2(ml.x - ref);
+    }
+#pragma unroll
+    for (int k = 16; k; k >>= 1) sum += __shfl_xor_sync(~0u, sum, k);
+  };
+
+  if (joins) {
+    const int unit_in_b = id % units_b;
+    const int h = unit_in_b / p.row_blocks, rb = unit_in_b % p.row_blocks;
+    const int r = (blockIdx.x % row_groups) * 4 + warp;
+    const int row = rb * kRows + r;
+    if (row >= n_rows) return;
+    size_t first, last;
+    slots_of(unit_in_b, first, last);
+    float mx, sum;
+    statistics(first, last, r, mx, sum);
+    const float ref = mx == -INFINITY ? 0.f : mx;
+    constexpr int V = D / 32;
+    float acc[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = 0.f;
+    for (size_t s = first; s <= last; s += 4) {
+      float x[4][V], a[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {  // four rows of loads under way at a time
+        const bool have = s + k <= last;
+        const size_t at = (have ? s + k : s) * kRows + r;
+        a[k] = have ? ptx::ex2(p.part_ml[at].x - ref) : 0.f;
+        const float* src = p.part_o + at * D + lane * V;
+        if constexpr (V == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(src);
+          x[k][0] = v.x;
+          x[k][1] = v.y;
+          x[k][V - 2] = v.z;
+          x[k][V - 1] = v.w;
+        } else {
+          const float2 v = *reinterpret_cast<const float2*>(src);
+          x[k][0] = v.x;
+          x[k][1] = v.y;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (s + k <= last)
+#pragma unroll
+          for (int i = 0; i < V; ++i) acc[i] = fmaf(x[k][i], a[k], acc[i]);
+    }
+    // a sum that is NaN (a query that is not finite) must stay NaN
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int t = row / p.group, hq = h * p.group + row % p.group;
+    uint16_t* dst = static_cast<uint16_t*>(p.o.data) + b * p.o.sb + t * p.o.st + hq * p.o.sh +
+                    lane * V;
+    if constexpr (V == 4)
+      *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<kDtype>(acc[0] * inv, acc[1] * inv),
+                                                  pack2<kDtype>(acc[V - 2] * inv, acc[V - 1] * inv));
+    else
+      *reinterpret_cast<uint32_t*>(dst) = pack2<kDtype>(acc[0] * inv, acc[1] * inv);
+    if (lane == 0 && p.lse != nullptr)
+      p.lse[(static_cast<size_t>(b) * p.heads + hq) * p.T + t] =
+          sum == 0.f ? -INFINITY : (mx + log2f(sum)) * 0.69314718055994531f;
+    return;
+  }
+
+  // ---- weights of rows j0 .. of KV head h
+  const int h = id % c.H;
+  const int j0 = static_cast<int>((blockIdx.x - join_blocks) % chunks) * kJoinKeys;
+  if (j0 >= held) return;
+  extern __shared__ float s_lse[];  // [score_rows]
+  for (int row = warp; row < p.score_rows; row += 4) {
+    float mx = 0.f, sum = 0.f;
+    if (row < n_rows) {
+      size_t first, last;
+      slots_of(h * p.row_blocks + row / kRows, first, last);
+      statistics(first, last, row % kRows, mx, sum);
+    }
+    // rows that are not there, or see nothing, add 0
+    if (lane == 0) s_lse[row] = row < n_rows && sum != 0.f ? mx + log2f(sum) : INFINITY;
+  }
+  __syncthreads();
+  const size_t plane = (static_cast<size_t>(b) * c.H + h) * c.N;
+  for (int j = j0 + threadIdx.x; j < min(j0 + kJoinKeys, held); j += 128) {
+    const float* src = p.scores + (plane + j) * p.score_rows;
+    float sum = 0.f;
+    for (int r = 0; r < p.score_rows; r += 2) {
+      const float2 x = *reinterpret_cast<const float2*>(src + r);
+      sum += ptx::ex2(x.x - s_lse[r]) + ptx::ex2(x.y - s_lse[r + 1]);
+    }
+    c.weight[plane + j] += sum;
+  }
+}
+
+}  // namespace sa

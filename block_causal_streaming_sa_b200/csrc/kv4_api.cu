@@ -3,12 +3,14 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <initializer_list>
 #include <string>
 
 #include "host_common.h"
 #include "kernels/kv4_attend_rows.cuh"
+#include "kernels/kv4_decode.cuh"
 #include "kernels/kv4_evict.cuh"
 #include "kernels/kv4_rows.cuh"
 
@@ -158,8 +160,119 @@ int check_heads(const sa_kv4_cache* c, int heads, int T) {
   return SA_OK;
 }
 
-size_t attend_bytes(const sa_kv4_cache* c, int heads, int T) {
-  return align_up(static_cast<size_t>(c->batch) * heads * T * sizeof(float), 256);
+constexpr int kMaxDevices = 64;
+
+// Number of SMs of the current device (asked once a device).
+int sm_count() {
+  static std::atomic<int> known[kMaxDevices];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 148;
+  n = known[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
+      n = 148;
+    known[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+// Lets `kernel` use its dynamic shared memory on the current device.
+template <auto kernel>
+bool allow_smem(int bytes) {
+  static std::atomic<bool> done[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
+  if (done[dev].load(std::memory_order_relaxed)) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
+      cudaSuccess)
+    return false;
+  done[dev].store(true, std::memory_order_relaxed);
+  return true;
+}
+
+// Launch that may begin while the kernel before it on the stream drains; the kernel
+// itself waits (griddepcontrol.wait) before it reads what that one wrote.
+template <typename... P, typename... A>
+void launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                  A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// How an attention is run: sizes that follow from the shape alone, so that the
+// workspace can be asked for ahead.
+struct AttendPlan {
+  bool few;        // few query rows: kv4_decode.cuh
+  int nt;          // query rows of a block / 8
+  int row_blocks;  // blocks of query rows per (sequence, KV head)
+  int score_rows;
+  long long blocks;  // of the decode kernel, at most
+  size_t off_o, off_ml, off_scores, total;
+};
+
+constexpr int kFewRows = 64;
+constexpr int kMostSms = 256;  // the workspace covers a grid of any GPU of this kind
+
+int decode_blocks_per_sm(int nt) { return nt == 1 ? 4 : nt == 2 ? 3 : 2; }
+
+AttendPlan plan_attend(const sa_kv4_cache* c, int heads, int T, bool weights) {
+  AttendPlan a{};
+  const int rows = heads / c->kv_heads * T, D = c->head_dim;
+  const size_t planes = static_cast<size_t>(c->batch) * c->kv_heads;
+  a.few = rows <= kFewRows;
+  size_t off = 0;
+  if (a.few) {
+    a.nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+    a.row_blocks = (rows + 8 * a.nt - 1) / (8 * a.nt);
+    a.blocks = static_cast<long long>(kMostSms) * decode_blocks_per_sm(a.nt);
+    const size_t slots = a.blocks + planes * a.row_blocks;
+    a.off_o = off;
+    off += align_up(slots * 8 * a.nt * D * sizeof(float), 256);
+    a.off_ml = off;
+    off += align_up(slots * 8 * a.nt * sizeof(float2), 256);
+    a.score_rows = (rows + 1) / 2 * 2;
+    a.off_scores = off;
+    if (weights) off += align_up(planes * c->capacity * a.score_rows * sizeof(float), 256);
+  } else {
+    a.off_scores = off;
+    off += align_up(static_cast<size_t>(c->batch) * heads * T * sizeof(float), 256);
+  }
+  a.total = off;
+  return a;
+}
+
+template <int D, int NT, int kDtype, bool kScores>
+bool launch_decode(const sa::Kv4AttendParams& p, cudaStream_t s) {
+  using S = sa::DecodeShape<D, NT>;
+  if (!allow_smem<sa::kv4_decode_kernel<D, NT, kDtype, kScores>>(S::kSmem)) return false;
+  const int blocks = std::min(sm_count(), kMostSms) * S::kBlocksPerSm;
+  sa::kv4_decode_kernel<D, NT, kDtype, kScores><<<blocks, 128, S::kSmem, s>>>(p);
+  const int join = p.c.B * p.c.H * p.row_blocks * (S::kRows / 4);
+  const int chunks = (p.c.N + sa::kJoinKeys - 1) / sa::kJoinKeys;
+  const int grid = join + (kScores ? p.c.B * p.c.H * chunks : 0);
+  launch_after(sa::kv4_join_kernel<D, S::kRows, kDtype>, dim3(grid), dim3(128),
+               p.score_rows * sizeof(float), s, p, blocks, join);
+  return true;
+}
+
+template <int D, int kDtype>
+bool launch_decode_nt(const sa::Kv4AttendParams& p, int nt, cudaStream_t s) {
+  if (p.add_weight)
+    return nt == 1   ? launch_decode<D, 1, kDtype, true>(p, s)
+           : nt == 2 ? launch_decode<D, 2, kDtype, true>(p, s)
+                     : launch_decode<D, 4, kDtype, true>(p, s);
+  return nt == 1   ? launch_decode<D, 1, kDtype, false>(p, s)
+         : nt == 2 ? launch_decode<D, 2, kDtype, false>(p, s)
+                   : launch_decode<D, 4, kDtype, false>(p, s);
 }
 
 size_t evict_bytes(const sa_kv4_cache* c) {
@@ -240,10 +353,9 @@ SA_API int sa_kv4_read(const sa_kv4_cache* c, int first, const sa_rows* K, const
 }
 
 SA_API size_t sa_kv4_attend_bytes(const sa_kv4_cache* c, int heads, int T, int add_weight) {
-  (void)add_weight;
   if (check_sizes(c) != SA_OK || T < 0 || T > kMaxTokens || check_heads(c, heads, T) != SA_OK)
     return 0;
-  return attend_bytes(c, heads, T);
+  return plan_attend(c, heads, T, add_weight != 0).total;
 }
 
 SA_API int sa_kv4_attend(const sa_kv4_cache* c, const sa_rows* Q, const sa_rows* O, int dtype,
@@ -265,8 +377,8 @@ SA_API int sa_kv4_attend(const sa_kv4_cache* c, const sa_rows* Q, const sa_rows*
   if (reinterpret_cast<uintptr_t>(lse) & 3u)
     return refuse(SA_ERR_INVALID_ARG, "lse must be 4-byte aligned");
   if (!device_memory(lse, device, "lse", &why)) return refuse(SA_ERR_INVALID_ARG, why);
-  if (int rc = check_workspace(workspace, workspace_bytes, attend_bytes(c, heads, T), device);
-      rc != SA_OK)
+  const AttendPlan plan = plan_attend(c, heads, T, add_weight != 0);
+  if (int rc = check_workspace(workspace, workspace_bytes, plan.total, device); rc != SA_OK)
     return rc;
   if (T == 0) return SA_OK;
   p.counts = counts;
@@ -276,9 +388,25 @@ SA_API int sa_kv4_attend(const sa_kv4_cache* c, const sa_rows* Q, const sa_rows*
   p.T = T;
   p.causal = causal != 0;
   p.scale_log2 = (scale > 0.f ? scale : 1.f / std::sqrt(static_cast<float>(D))) * 1.44269504f;
-  p.lse2 = static_cast<float*>(workspace);
+  p.add_weight = add_weight != 0;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.row_blocks = plan.row_blocks;
+  p.part_o = reinterpret_cast<float*>(ws + plan.off_o);
+  p.part_ml = reinterpret_cast<float2*>(ws + plan.off_ml);
+  p.scores = reinterpret_cast<float*>(ws + plan.off_scores);
+  p.score_rows = plan.score_rows;
   DeviceGuard guard(device);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (plan.few) {
+    const bool ok = D == 128 ? (dtype == SA_DTYPE_FP16
+                                    ? launch_decode_nt<128, SA_DTYPE_FP16>(p, plan.nt, s)
+                                    : launch_decode_nt<128, SA_DTYPE_BF16>(p, plan.nt, s))
+                             : (dtype == SA_DTYPE_FP16
+                                    ? launch_decode_nt<64, SA_DTYPE_FP16>(p, plan.nt, s)
+                                    : launch_decode_nt<64, SA_DTYPE_BF16>(p, plan.nt, s));
+    if (!ok) return refuse(SA_ERR_CUDA, "shared memory of the attention kernel");
+    return launched("attention");
+  }
   const dim3 grid((T + 3) / 4, heads, p.c.B), wgrid(p.c.N / 128, p.c.H, p.c.B);
   auto run = [&](auto attend, auto weights) {
     attend<<<grid, 128, 0, s>>>(p);
