@@ -1,0 +1,670 @@
+// Attention of many query rows over a 4-bit cache: chunks and prompts.
+//
+// Bound by the matrix and the exponential units: 4 D flop and one exponential per
+// (query row, cache row). The design is the chunk-cache attention's (two query tiles
+// of 128 rows ping-pong over every K / V tile, S and O in tensor memory, P written
+// over S), with these differences:
+//  * K and V arrive as codes. A warpgroup of its own reads them from global memory
+//    one tile ahead into registers, converts and scales them (exact in fp16) and
+//    stores them in the swizzled layout the products read, 350 instructions a thread
+//    and tile pair next to the ~2050 cycles of its four products. Converting on the
+//    fly reads 288 bytes a row and head instead of 512 + the 800 that a 16-bit copy
+//    made ahead would move, and needs no copy of the cache.
+//  * Queries are staged once per call (kv4_stage_kernel): scaled to fp16 by a power
+//    of two per row and stored as the 128-row tiles' shared memory images, so a tile
+//    is one bulk copy whatever the tensor's strides are.
+//  * Work is one line of (query tile pair, key tile) steps cut into equal ranges, one
+//    a block, so neither causal masks, ragged lengths nor the last round leave SMs
+//    idle. A block writes whole pairs to O; of a pair that lies in several ranges
+//    each block leaves an fp32 partial result, at most two a block, which
+//    kv4_chunk_join_kernel merges in the order of the ranges.
+//  * Registers: 512 threads launched at 128; softmax warpgroups 192, conversion 88,
+//    the issuing warp's 40 (their sum is the launch's).
+#pragma once
+
+#include "kv4_params.cuh"
+
+namespace sa {
+
+template <int D>
+struct ChunkShape {
+  static constexpr int BM = 128, BN = 128;
+  static constexpr int KBLK = D / 64;       // 128-byte swizzle atoms of a row
+  static constexpr int kTile = BM * D * 2;  // bytes of a Q, K or V tile
+  static constexpr int kBox = BN * 128;     // bytes of 64 columns of a tile
+  static constexpr int NSTAGE = 4;          // K, V, K, V
+  static constexpr int kThreads = 512;
+  static constexpr int kRegsSoftmax = 192, kRegsConvert = 88, kRegsIssue = 40;
+  static_assert(2 * kRegsSoftmax + kRegsConvert + kRegsIssue <= 512, "launched at 128 each");
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffKV = 2 * kTile;
+  static constexpr int kOffBar = kOffKV + NSTAGE * kTile;
+  static constexpr int kSmem = kOffBar + 256 + 1024;  // + alignment slack
+  static constexpr int kTmemCols = 512;
+  static constexpr uint32_t kIdescQK = ptx::idesc_f32acc(BM, BN, 0, 0);  // fp16
+  static constexpr uint32_t kIdescPV = ptx::idesc_f32acc(BM, D, 0, 1);   // fp16, V MN-major
+  __host__ __device__ static constexpr int col_s(int i) { return i * 128; }
+  __host__ __device__ static constexpr int col_p(int i) { return i * 128 + 64; }
+  __host__ __device__ static constexpr int col_o(int i) { return 256 + i * D; }
+  __host__ __device__ static constexpr int FULL(int s) { return s; }
+  __host__ __device__ static constexpr int EMPTY(int s) { return NSTAGE + s; }
+  __host__ __device__ static constexpr int SFULL(int i) { return 2 * NSTAGE + i; }
+  __host__ __device__ static constexpr int PFULL(int i) { return 2 * NSTAGE + 2 + i; }
+  __host__ __device__ static constexpr int OFINAL(int i) { return 2 * NSTAGE + 4 + i; }
+  __host__ __device__ static constexpr int QLOAD(int i) { return 2 * NSTAGE + 6 + i; }
+  __host__ __device__ static constexpr int DRAIN() { return 2 * NSTAGE + 8; }
+};
+
+// Offset of 16-byte piece c of row r in a 128-byte-swizzled K-major tile of 128 rows.
+__device__ __forceinline__ uint32_t tile_offset(int r, int c) {
+  return static_cast<uint32_t>((c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t x, uint32_t y, uint32_t z,
+                                       uint32_t w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z),
+               "r"(w)
+               : "memory");
+}
+
+// Key tiles that pair `pair` (query rows 256 pair ..) of sequence b goes through.
+__device__ __forceinline__ int pair_tiles(const Kv4AttendParams& p, int held, int n_tok, int pair) {
+  const int n_rows = n_tok * p.group;
+  if (256 * pair >= n_rows) return 0;
+  const int last = min(256 * pair + 256, n_rows) - 1;
+  return (rows_seen(p, held, n_tok, last / p.group) + 127) / 128;
+}
+
+// Queries to fp16 tiles, per-row scales, and the schedule. Block (x, h, b) stages
+// tile x; block (n_tiles, 0, 0) sums up the steps: line[b] = steps before sequence b,
+// pre[b][pair] = steps of one head of b before that pair (last entry: of all pairs).
+template <int D, int kDtype>
+__global__ void __launch_bounds__(256)
+    kv4_stage_kernel(const __grid_constant__ Kv4AttendParams p) {
+  constexpr int C = D / 8;  // 16-byte pieces of a row
+  const Kv4& c = p.c;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (static_cast<int>(blockIdx.x) == p.q_tiles) {
+    if (blockIdx.y != 0 || blockIdx.z != 0) return;
+    __shared__ int warp_sum[8];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long before = 0;
+    for (int b = 0; b < c.B; ++b) {
+      const int held = rows_held(c, b), n_tok = tokens_of(p.counts, b, p.T);
+      if (threadIdx.x == 0) check_order(p, b, n_tok);
+      int sum = 0;
+      int* pre = p.pre + static_cast<size_t>(b) * (p.pairs + 1);
+      for (int q0 = 0; q0 < p.pairs; q0 += 256) {
+        const int q = q0 + threadIdx.x;
+        const int v = q < p.pairs ? pair_tiles(p, held, n_tok, q) : 0;
+        int x = v;
+#pragma unroll
+        for (int k = 1; k < 32; k <<= 1) {
+          const int y = __shfl_up_sync(~0u, x, k);
+          if (lane >= k) x += y;
+        }
+        if (lane == 31) warp_sum[warp] = x;
+        __syncthreads();
+        int base = sum;
+        for (int w = 0; w < 8; ++w) {
+          if (w < warp) base += warp_sum[w];
+          sum += warp_sum[w];
+        }
+        if (q < p.pairs) pre[q] = base + x - v;
+        __syncthreads();
+      }
+      if (threadIdx.x == 0) {
+        pre[p.pairs] = sum;
+        p.line[b] = before;
+      }
+      before += static_cast<long long>(sum) * c.H;
+    }
+    if (threadIdx.x == 0) p.line[c.B] = before;
+    return;
+  }
+  const int b = blockIdx.z, h = blockIdx.y, tile = blockIdx.x;
+  const int held = rows_held(c, b), n_tok = tokens_of(p.counts, b, p.T);
+  const int n_rows = n_tok * p.group;
+  if (tile * 128 >= n_rows) return;
+  const bool empty = pair_tiles(p, held, n_tok, tile / 2) == 0;  // no block goes there
+  const size_t tile_id = (static_cast<size_t>(b) * c.H + h) * p.q_tiles + tile;
+  uint8_t* dst = p.q_img + tile_id * (128 * D * 2);
+  for (int i = threadIdx.x; i < 128 * C; i += 256) {
+    const int r = i / C, piece = i % C, row = tile * 128 + r;
+    const int t = row / p.group, hq = h * p.group + row % p.group;
+    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+    if (row < n_rows)
+      w = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q.data) +
+                                               b * p.q.sb + t * p.q.st + hq * p.q.sh) +
+                piece);
+    const float2 v[4] = {unpack2<kDtype>(w.x), unpack2<kDtype>(w.y), unpack2<kDtype>(w.z),
+                         unpack2<kDtype>(w.w)};
+    float amax = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) amax = fmaxf(amax, fmaxf(fabsf(v[k].x), fabsf(v[k].y)));
+#pragma unroll
+    for (int k = 1; k < C; k <<= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, k));
+    const float f = row_factor(amax);
+    uint32_t x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] = pack2<SA_DTYPE_FP16>(v[k].x * f, v[k].y * f);
+    *reinterpret_cast<uint4*>(dst + tile_offset(r, piece)) = make_uint4(x[0], x[1], x[2], x[3]);
+    if (piece == 0) p.row_scale[tile_id * 128 + r] = row < n_rows ? p.scale_log2 / f : 0.f;
+    if (row >= n_rows) {
+      if (piece == 0) p.row_lse[tile_id * 128 + r] = INFINITY;  // such rows draw no weight
+    } else if (empty) {
+      uint16_t* o = static_cast<uint16_t*>(p.o.data) + b * p.o.sb + t * p.o.st + hq * p.o.sh;
+      *reinterpret_cast<uint4*>(o + piece * 8) = make_uint4(0u, 0u, 0u, 0u);
+      if (piece == 0) {
+        if (p.lse != nullptr)
+          p.lse[(static_cast<size_t>(b) * p.heads + hq) * p.T + t] = -INFINITY;
+        p.row_lse[tile_id * 128 + r] = INFINITY;
+      }
+    }
+  }
+}
+
+// A walk along the line of steps: the pairs of a range, each with its key tiles.
+struct ChunkWalk {
+  long long at, stop;  // steps of the line
+  int b, h, pair;
+  int t0, t1, n;  // key tiles [t0, t1) of n
+
+  __device__ __forceinline__ void start(const Kv4AttendParams& p, long long from, long long to) {
+    at = from;
+    stop = to;
+    b = h = pair = t0 = t1 = n = 0;
+  }
+  // The next pair of the range; false at its end.
+  __device__ __forceinline__ bool next(const Kv4AttendParams& p) {
+    if (at >= stop) return false;
+    while (at >= p.line[b + 1]) ++b;
+    const int* pre = p.pre + static_cast<size_t>(b) * (p.pairs + 1);
+    const int per_head = pre[p.pairs];
+    const long long in_b = at - p.line[b];
+    h = static_cast<int>(in_b / per_head);
+    const int in_h = static_cast<int>(in_b % per_head);
+    int lo = 0, hi = p.pairs;  // pre[lo] <= in_h < pre[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (pre[mid] <= in_h)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    // of pairs without steps that share a start, the last is the one with steps
+    pair = lo;
+    n = pre[pair + 1] - pre[pair];
+    t0 = in_h - pre[pair];
+    t1 = static_cast<int>(min(static_cast<long long>(n), t0 + (stop - at)));
+    at += t1 - t0;
+    return true;
+  }
+};
+
+__device__ __forceinline__ long long chunk_share(const Kv4AttendParams& p, int blocks) {
+  return (p.line[p.c.B] + blocks - 1) / blocks;
+}
+
+// Where a block leaves the partial result of a pair: a range that begins inside a
+// pair (t0 > 0) can do so once, a range that ends inside one it began (t0 = 0) too.
+__device__ __forceinline__ size_t partial_slot(int block, int t0) {
+  return 2 * static_cast<size_t>(block) + (t0 > 0 ? 0 : 1);
+}
+
+// One query row's result: O / l to its place, or the partial row. A function of its
+// own so that its registers do not add to the score loop's.
+template <int D, int kDtype>
+__device__ __noinline__ void chunk_epilogue(const Kv4AttendParams& p, uint32_t tO, float m,
+                                            float lsum, bool whole, size_t slot, int i, int r,
+                                            int b, int h, int row, int n_rows) {
+  if (!whole) {
+    float4* dst = reinterpret_cast<float4*>(p.part_o) + slot * (D / 4) * 256 + i * 128 + r;
+#pragma unroll 1
+    for (int j = 0; j < D / 32; ++j) {
+      uint32_t o[32];
+      ptx::tmem_ld32(tO + j * 32, o);
+      ptx::tmem_wait_ld();
+#pragma unroll
+      for (int k = 0; k < 32; k += 4)  // [D / 4][256 rows][4]: a warp's stores are contiguous
+        dst[static_cast<size_t>(j * 8 + k / 4) * 256] =
+            make_float4(__uint_as_float(o[k]), __uint_as_float(o[k + 1]),
+                        __uint_as_float(o[k + 2]), __uint_as_float(o[k + 3]));
+    }
+    p.part_ml[slot * 256 + i * 128 + r] = make_float2(m, lsum);
+    return;
+  }
+  const float inv = lsum == 0.f ? 0.f : 1.f / lsum;  // NaN stays NaN
+  const int t = row / p.group, hq = h * p.group + row % p.group;
+  uint16_t* dst = static_cast<uint16_t*>(p.o.data) + b * p.o.sb + t * p.o.st + hq * p.o.sh;
+#pragma unroll 1
+  for (int j = 0; j < D / 32; ++j) {
+    uint32_t o[32];
+    ptx::tmem_ld32(tO + j * 32, o);
+    ptx::tmem_wait_ld();
+    if (row < n_rows)
+#pragma unroll
+      for (int k = 0; k < 32; k += 8)
+        *reinterpret_cast<uint4*>(dst + j * 32 + k) = make_uint4(
+            pack2<kDtype>(__uint_as_float(o[k]) * inv, __uint_as_float(o[k + 1]) * inv),
+            pack2<kDtype>(__uint_as_float(o[k + 2]) * inv, __uint_as_float(o[k + 3]) * inv),
+            pack2<kDtype>(__uint_as_float(o[k + 4]) * inv, __uint_as_float(o[k + 5]) * inv),
+            pack2<kDtype>(__uint_as_float(o[k + 6]) * inv, __uint_as_float(o[k + 7]) * inv));
+  }
+  if (row < n_rows) {
+    const float lse2 = lsum == 0.f ? -INFINITY : m + log2f(lsum);
+    if (p.lse != nullptr)
+      p.lse[(static_cast<size_t>(b) * p.heads + hq) * p.T + t] = lse2 * 0.69314718055994531f;
+    p.row_lse[((static_cast<size_t>(b) * p.c.H + h) * p.q_tiles) * 128 + row] =
+        lsum == 0.f ? INFINITY : lse2;
+  }
+}
+
+// Codes of a thread's part of one K or V tile, read ahead: 16-byte pieces (32 codes),
+// piece i * 128 + thread of the tile's 128 * D / 32, with their two scales.
+template <int D>
+struct ConvertRegs {
+  static constexpr int N = D / 32;
+  uint4 w[N];
+  uint32_t sc[N];
+};
+
+template <int D>
+__device__ __forceinline__ void convert_load(ConvertRegs<D>& x, const uint8_t* codes,
+                                             const uint8_t* scales, size_t row0, int tid) {
+  constexpr int P = D / 32;  // pieces of a row
+  const uint4* src = reinterpret_cast<const uint4*>(codes + row0 * (D / 2));
+  const uint16_t* sc = reinterpret_cast<const uint16_t*>(scales + row0 * (D / 16));
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    x.w[i] = __ldg(src + i * 128 + tid);
+    x.sc[i] = __ldg(sc + i * 128 + tid);
+  }
+}
+
+// Into the swizzled tile; rows from `valid` on become zeros (what lies there may be
+// anything, and a scale may be NaN).
+template <int D>
+__device__ __forceinline__ void convert_store(const ConvertRegs<D>& x, uint32_t tile, int tid,
+                                              int valid) {
+  constexpr int P = D / 32;
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int row = (i * 128 + tid) / P, piece = (i * 128 + tid) % P;
+    const uint32_t bytes = row < valid ? x.sc[i] : 0u;
+    const uint32_t s0 = scale_f16x2(bytes & 255u), s1 = scale_f16x2(bytes >> 8);
+    const uint32_t w[4] = {x.w[i].x, x.w[i].y, x.w[i].z, x.w[i].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t h[4];
+      codes_to_f16(w[j], h);
+      const uint32_t s = j < 2 ? s0 : s1;
+      sts128(tile + tile_offset(row, piece * 4 + j), mul_f16x2(h[0], s), mul_f16x2(h[1], s),
+             mul_f16x2(h[2], s), mul_f16x2(h[3], s));
+    }
+  }
+}
+
+template <int D, int kDtype>
+__global__ void __launch_bounds__(512, 1)
+    kv4_chunk_kernel(const __grid_constant__ Kv4AttendParams p) {
+  using S = ChunkShape<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const Kv4& c = p.c;
+  const uint32_t raw = ptx::smem_addr(smem_raw);
+  uint8_t* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+  const uint32_t sbase = ptx::smem_addr(smem);
+  auto bar = [&](int i) { return sbase + S::kOffBar + 8u * static_cast<uint32_t>(i); };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kOffBar + 240);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kOffBar + 248);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::NSTAGE; ++s) {
+      ptx::mbar_init(bar(S::FULL(s)), 4);  // the four converting warps
+      ptx::mbar_init(bar(S::EMPTY(s)), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(bar(S::SFULL(i)), 1);
+      ptx::mbar_init(bar(S::PFULL(i)), 128);
+      ptx::mbar_init(bar(S::OFINAL(i)), 1);
+      ptx::mbar_init(bar(S::QLOAD(i)), 1);
+    }
+    ptx::mbar_init(bar(S::DRAIN()), 1);
+    *abort_flag = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 12) {
+    ptx::tmem_alloc(ptx::smem_addr(tmem_slot), S::kTmemCols);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // staged queries and schedule
+
+  const long long share = chunk_share(p, gridDim.x);
+  ChunkWalk walk;
+  walk.start(p, min(blockIdx.x * share, p.line[c.B]), min((blockIdx.x + 1) * share, p.line[c.B]));
+
+  if (warp >= 12) {
+    ptx::setmaxnreg_dec<S::kRegsIssue>();
+    if (warp == 12 && lane == 0) {
+      // ------------------------------------------------------------ MMA issuer
+      int stage = 0;
+      uint32_t phase = 0, pf_phase[2] = {0u, 0u};
+      uint32_t q_units[2] = {0u, 0u};  // pairs so far that used query tile i
+      bool ok = true;
+      auto take = [&](int& s_out) -> bool {
+        s_out = stage;
+        const bool r = ptx::mbar_wait(bar(S::FULL(stage)), phase, abort_flag, c.status);
+        if (++stage == S::NSTAGE) {
+          stage = 0;
+          phase ^= 1u;
+        }
+        return r;
+      };
+      auto issue_s = [&](int i, int sk) {
+        const uint32_t qa = sbase + S::kOffQ + i * S::kTile;
+        const uint32_t kb = sbase + S::kOffKV + sk * S::kTile;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * S::kBox + (kk & 3) * 32;
+          ptx::umma_ss(tmem + S::col_s(i), ptx::smem_desc_sw128(qa + off, 16, 1024),
+                       ptx::smem_desc_sw128(kb + off, 16, 1024), S::kIdescQK, kk > 0 ? 1u : 0u);
+        }
+        ptx::umma_commit(bar(S::SFULL(i)));
+      };
+      auto issue_pv = [&](int i, int sv, bool accumulate) {
+        const uint32_t vb = sbase + S::kOffKV + sv * S::kTile;
+#pragma unroll
+        for (int kk = 0; kk < S::BN / 16; ++kk)
+          ptx::umma_ts(tmem + S::col_o(i), tmem + S::col_p(i) + kk * 8,
+                       ptx::smem_desc_sw128(vb + kk * 16 * 128, S::kBox, 1024), S::kIdescPV,
+                       (accumulate || kk > 0) ? 1u : 0u);
+      };
+      while (ok && walk.next(p)) {
+        const int n_rows = tokens_of(p.counts, walk.b, p.T) * p.group;
+        const int tiles = n_rows > walk.pair * 256 + 128 ? 2 : 1;
+        const size_t tile_id =
+            (static_cast<size_t>(walk.b) * c.H + walk.h) * p.q_tiles + 2 * walk.pair;
+        for (int i = 0; i < tiles && ok; ++i) {
+          // every product that read the previous tile is done once its O is final
+          if (q_units[i] > 0)
+            ok = ptx::mbar_wait(bar(S::OFINAL(i)), (q_units[i] - 1) & 1, abort_flag, c.status);
+          if (!ok) break;
+          ptx::mbar_arrive_expect_tx(bar(S::QLOAD(i)), S::kTile);
+          asm volatile(
+              "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, "
+              "[%3];" ::"r"(sbase + S::kOffQ + i * S::kTile),
+              "l"(p.q_img + (tile_id + i) * S::kTile), "r"(S::kTile), "r"(bar(S::QLOAD(i)))
+              : "memory");
+          ++q_units[i];
+        }
+        int sk = 0, sv = 0;
+        if (!ok || !take(sk)) {
+          ok = false;
+          break;
+        }
+        ptx::tc_fence_after();
+        for (int i = 0; i < tiles && ok; ++i) {
+          ok = ptx::mbar_wait(bar(S::QLOAD(i)), (q_units[i] - 1) & 1, abort_flag, c.status);
+          if (ok) issue_s(i, sk);
+        }
+        if (!ok) break;
+        ptx::umma_commit(bar(S::EMPTY(sk)));
+        for (int t = walk.t0; ok && t < walk.t1; ++t) {
+          const bool more = t + 1 < walk.t1;
+          if (!take(sv) || (more && !take(sk))) {
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after();
+          for (int i = 0; i < tiles; ++i) {
+            if (!ptx::mbar_wait(bar(S::PFULL(i)), pf_phase[i], abort_flag, c.status)) {
+              ok = false;
+              break;
+            }
+            pf_phase[i] ^= 1u;
+            ptx::tc_fence_after();
+            issue_pv(i, sv, t > walk.t0);
+            if (i == tiles - 1) ptx::umma_commit(bar(S::EMPTY(sv)));
+            if (more)
+              issue_s(i, sk);
+            else
+              ptx::umma_commit(bar(S::OFINAL(i)));
+          }
+          if (ok && more) ptx::umma_commit(bar(S::EMPTY(sk)));
+        }
+      }
+      // every product finishes before tensor memory is released, and query copies land
+      // before the block can end (also after an abort)
+      volatile int none = 0;
+      ptx::umma_commit(bar(S::DRAIN()));
+      ptx::mbar_wait(bar(S::DRAIN()), 0, &none, c.status);
+      for (int i = 0; i < 2; ++i)
+        if (q_units[i] > 0)
+          ptx::mbar_wait(bar(S::QLOAD(i)), (q_units[i] - 1) & 1, &none, c.status);
+    }
+  } else if (warp >= 8) {
+    ptx::setmaxnreg_dec<S::kRegsConvert>();
+    // ------------------------------------------------------------ conversion
+    const int tid = threadIdx.x - 256;
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    auto publish = [&](const ConvertRegs<D>& x, int valid) {
+      if (!__all_sync(~0u, ptx::mbar_wait(bar(S::EMPTY(stage)), phase ^ 1u, abort_flag,
+                                          c.status))) {
+        ok = false;
+        return;
+      }
+      convert_store<D>(x, sbase + S::kOffKV + stage * S::kTile, tid, valid);
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar(S::FULL(stage)));
+      if (++stage == S::NSTAGE) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    };
+    while (ok && walk.next(p)) {
+      const int held = rows_held(c, walk.b);
+      const size_t plane = (static_cast<size_t>(walk.b) * c.H + walk.h) * c.N;
+      ConvertRegs<D> kx, vx;
+      convert_load<D>(kx, c.k_codes, c.k_scales, plane + walk.t0 * 128, tid);
+      convert_load<D>(vx, c.v_codes, c.v_scales, plane + walk.t0 * 128, tid);
+      for (int t = walk.t0; ok && t < walk.t1; ++t) {
+        const size_t next = plane + (t + 1) * 128;
+        publish(kx, held - t * 128);
+        if (!ok) break;
+        if (t + 1 < walk.t1) convert_load<D>(kx, c.k_codes, c.k_scales, next, tid);
+        publish(vx, held - t * 128);
+        if (t + 1 < walk.t1) convert_load<D>(vx, c.v_codes, c.v_scales, next, tid);
+      }
+    }
+  } else {
+    ptx::setmaxnreg_inc<S::kRegsSoftmax>();
+    // ------------------------------------------------------------ softmax
+    const int i = warp >> 2;       // query tile of this warpgroup
+    const int quarter = warp & 3;  // tensor memory lanes this warp may access
+    const int r = quarter * 32 + lane;
+    const uint32_t t_lane = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t tS = tmem + t_lane + S::col_s(i);
+    const uint32_t tO = tmem + t_lane + S::col_o(i);
+    uint32_t s_phase = 0, units = 0;
+    bool ok = true;
+    while (ok && walk.next(p)) {
+      const int held = rows_held(c, walk.b), n_tok = tokens_of(p.counts, walk.b, p.T);
+      const int n_rows = n_tok * p.group;
+      if (i == 1 && n_rows <= walk.pair * 256 + 128) continue;
+      const int row = walk.pair * 256 + i * 128 + r;
+      const int end = row < n_rows ? rows_seen(p, held, n_tok, row / p.group) : held;
+      const float sl =
+          p.row_scale[((static_cast<size_t>(walk.b) * c.H + walk.h) * p.q_tiles) * 128 + row];
+      float m = -INFINITY, lsum = 0.f;
+      for (int t = walk.t0; t < walk.t1; ++t) {
+        if (!__all_sync(~0u, ptx::mbar_wait(bar(S::SFULL(i)), s_phase, abort_flag, c.status))) {
+          ok = false;
+          break;
+        }
+        s_phase ^= 1u;
+        ptx::tc_fence_after();
+        uint32_t sr[4][32];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) ptx::tmem_ld32(tS + j * 32, sr[j]);
+        ptx::tmem_wait_ld();
+        const int hi = end - t * 128;
+        if (hi < 128) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (j * 32 + k >= hi) sr[j][k] = __float_as_uint(-INFINITY);
+        }
+        float mx8[8];
+#pragma unroll
+        for (int a = 0; a < 8; ++a) mx8[a] = __uint_as_float(sr[0][a]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int k = 0; k < 32; k += 2)
+            if (j > 0 || k >= 8)
+              mx8[(k >> 1) & 7] = ptx::fmax3(mx8[(k >> 1) & 7], __uint_as_float(sr[j][k]),
+                                             __uint_as_float(sr[j][k + 1]));
+        const float mx = fmaxf(ptx::fmax3(mx8[0], mx8[1], mx8[2]),
+                               fmaxf(ptx::fmax3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
+        const float m_new = fmaxf(m, mx * sl);
+        const bool need = m_new > m + 8.0f;
+        float alpha = 1.f;
+        if (need) {
+          alpha = ptx::ex2(m - m_new);
+          m = m_new;
+        }
+        // a row can meet a tile wholly behind its last key before any it sees
+        const float nm = m == -INFINITY ? 0.f : -m;
+        float rs8[8];
+#pragma unroll
+        for (int a = 0; a < 8; ++a) rs8[a] = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            float x0, x1;
+            ptx::ffma2(x0, x1, __uint_as_float(sr[j][2 * k]), __uint_as_float(sr[j][2 * k + 1]),
+                       sl, sl, nm, nm);
+            const float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1);
+            const int a = (k & 3) * 2;
+            ptx::fadd2(rs8[a], rs8[a + 1], rs8[a], rs8[a + 1], p0, p1);
+            pk[k] = pack2<SA_DTYPE_FP16>(p0, p1);
+          }
+          ptx::tmem_st16(tS + 64 + j * 16, pk);
+        }
+        lsum = lsum * alpha +
+               (((rs8[0] + rs8[1]) + (rs8[2] + rs8[3])) + ((rs8[4] + rs8[5]) + (rs8[6] + rs8[7])));
+        // the first tile's P V overwrote O; a later growth of the maximum rescales it
+        if (__any_sync(~0u, need && t > walk.t0)) {
+#pragma unroll
+          for (int j = 0; j < D / 32; ++j) {
+            uint32_t o[32];
+            ptx::tmem_ld32(tO + j * 32, o);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+            ptx::tmem_st32(tO + j * 32, o);
+          }
+        }
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(bar(S::PFULL(i)));
+      }
+      if (!ok) break;
+      if (!__all_sync(~0u, ptx::mbar_wait(bar(S::OFINAL(i)), units & 1, abort_flag, c.status)))
+        break;
+      ++units;
+      ptx::tc_fence_after();
+      chunk_epilogue<D, kDtype>(p, tO, m, lsum, walk.t0 == 0 && walk.t1 == walk.n,
+                                partial_slot(blockIdx.x, walk.t0), i, r, walk.b, walk.h, row,
+                                n_rows);
+      ptx::tc_fence_before();
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  if (warp == 12) ptx::tmem_dealloc(tmem, S::kTmemCols);
+}
+
+// Merge of the pairs that lie in several blocks' ranges: block x takes the pair in
+// which range x begins, if it begins inside one and no earlier range does. A thread
+// per query row, 32 rows (blockIdx.y) of the pair's 256.
+template <int D, int kDtype>
+__global__ void __launch_bounds__(128)
+    kv4_chunk_join_kernel(const __grid_constant__ Kv4AttendParams p, int blocks) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Kv4& c = p.c;
+  const long long share = chunk_share(p, blocks), total = p.line[c.B];
+  const long long from = (blockIdx.x + 1) * share;
+  if (from >= total) return;
+  ChunkWalk w;
+  w.start(p, from, total);
+  w.next(p);
+  const long long begin = from - w.t0, end = begin + w.n;  // the pair's steps
+  if (w.t0 == 0 || from - share > begin) return;  // not split here, or an earlier block's
+  const int first = static_cast<int>(begin / share), last = static_cast<int>((end - 1) / share);
+  const int n_tok = tokens_of(p.counts, w.b, p.T), n_rows = n_tok * p.group;
+  // four threads a row, D / 4 values each: r = row in the pair
+  const int r = blockIdx.y * 32 + (threadIdx.x & 31), part = threadIdx.x >> 5;
+  const int row = w.pair * 256 + r;
+  if (row >= n_rows) return;
+  auto slot_of = [&](int block) {
+    return partial_slot(block, block == first && first * share <= begin ? 0 : 1);
+  };
+  float mx = -INFINITY;
+  for (int k = first; k <= last; ++k) mx = fmaxf(mx, p.part_ml[slot_of(k) * 256 + r].x);
+  const float ref = mx == -INFINITY ? 0.f : mx;
+  float sum = 0.f;
+  constexpr int V = D / 16;  // float4 of a thread
+  float4 acc[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k = first; k <= last; ++k) {
+    const size_t slot = slot_of(k);
+    const float2 ml = p.part_ml[slot * 256 + r];
+    const float a = ptx::ex2(ml.x - ref);
+    sum += ml.y * a;
+    const float4* src =
+        reinterpret_cast<const float4*>(p.part_o) + slot * (D / 4) * 256 + part * V * 256 + r;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const float4 x = src[j * 256];
+      acc[j].x = fmaf(x.x, a, acc[j].x);
+      acc[j].y = fmaf(x.y, a, acc[j].y);
+      acc[j].z = fmaf(x.z, a, acc[j].z);
+      acc[j].w = fmaf(x.w, a, acc[j].w);
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int t = row / p.group, hq = w.h * p.group + row % p.group;
+  uint16_t* dst = static_cast<uint16_t*>(p.o.data) + w.b * p.o.sb + t * p.o.st + hq * p.o.sh +
+                  part * (D / 4);
+#pragma unroll
+  for (int j = 0; j < V; j += 2)
+    *reinterpret_cast<uint4*>(dst + 4 * j) =
+        make_uint4(pack2<kDtype>(acc[j].x * inv, acc[j].y * inv),
+                   pack2<kDtype>(acc[j].z * inv, acc[j].w * inv),
+                   pack2<kDtype>(acc[j + 1].x * inv, acc[j + 1].y * inv),
+                   pack2<kDtype>(acc[j + 1].z * inv, acc[j + 1].w * inv));
+  if (part == 0) {
+    const float lse2 = sum == 0.f ? -INFINITY : mx + log2f(sum);
+    if (p.lse != nullptr)
+      p.lse[(static_cast<size_t>(w.b) * p.heads + hq) * p.T + t] = lse2 * 0.69314718055994531f;
+    p.row_lse[((static_cast<size_t>(w.b) * c.H + w.h) * p.q_tiles) * 128 + row] =
+        sum == 0.f ? INFINITY : lse2;
+  }
+}
+
+}  // namespace sa

@@ -22,6 +22,13 @@ struct Kv4AttendParams {
   float2* part_ml; // [slot][rows of a block]: maximum (base 2), sum
   float* scores;   // [B][H][N][score_rows], base 2
   int score_rows;
+  // many query rows (kv4_chunk.cuh)
+  int q_tiles, pairs;  // tiles of 128 query rows per (sequence, KV head), and pairs of them
+  uint8_t* q_img;      // [B][H][q_tiles] shared memory images of the fp16 query tiles
+  float* row_scale;    // [B][H][q_tiles * 128]: score factor of a staged row
+  float* row_lse;      // the same: base-2 log-sum-exp, +inf where no weight is drawn
+  long long* line;     // [B + 1]
+  int* pre;            // [B][pairs + 1]
 };
 
 // Rows that query token t of sequence b reads.

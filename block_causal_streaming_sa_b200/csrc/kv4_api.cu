@@ -10,6 +10,7 @@
 
 #include "host_common.h"
 #include "kernels/kv4_attend_rows.cuh"
+#include "kernels/kv4_chunk.cuh"
 #include "kernels/kv4_decode.cuh"
 #include "kernels/kv4_evict.cuh"
 #include "kernels/kv4_rows.cuh"
@@ -155,7 +156,9 @@ constexpr int kMaxTokens = 1 << 24;
 int check_heads(const sa_kv4_cache* c, int heads, int T) {
   if (heads < 1 || heads % c->kv_heads != 0)
     return refuse(SA_ERR_INVALID_ARG, "heads must be a multiple of kv_heads");
-  if (heads > kMaxGridYZ || 1LL * (heads / c->kv_heads) * T > (1LL << 30))
+  const long long rows = 1LL * (heads / c->kv_heads) * T;
+  if (heads > kMaxGridYZ || rows > (1LL << 30) ||
+      (rows + 255) / 256 * (c->capacity / 128) > INT32_MAX)
     return refuse(SA_ERR_UNSUPPORTED, "too many query rows");
   return SA_OK;
 }
@@ -176,13 +179,18 @@ int sm_count() {
   return n;
 }
 
-// Lets `kernel` use its dynamic shared memory on the current device.
+// Lets `kernel` use its dynamic shared memory on the current device. regs > 0: the
+// register count its split between warpgroups assumes; with fewer at launch a
+// warpgroup would wait for registers that do not exist, so such a build is refused.
 template <auto kernel>
-bool allow_smem(int bytes) {
+bool allow_smem(int bytes, int regs = 0) {
   static std::atomic<bool> done[kMaxDevices];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
   if (done[dev].load(std::memory_order_relaxed)) return true;
+  cudaFuncAttributes fa;
+  if (regs > 0 && (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess || fa.numRegs != regs))
+    return false;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
       cudaSuccess)
     return false;
@@ -216,11 +224,15 @@ struct AttendPlan {
   int row_blocks;  // blocks of query rows per (sequence, KV head)
   int score_rows;
   long long blocks;  // of the decode kernel, at most
-  size_t off_o, off_ml, off_scores, total;
+  size_t off_o, off_ml, off_scores;
+  // many query rows: kv4_chunk.cuh
+  int q_tiles, pairs;
+  size_t off_q, off_scale, off_lse, off_line, off_pre;
+  size_t total;
 };
 
 constexpr int kFewRows = 64;
-constexpr int kMostSms = 256;  // the workspace covers a grid of any GPU of this kind
+constexpr int kMostSms = 160;  // the workspace covers a grid of any GPU of this kind
 
 int decode_blocks_per_sm(int nt) { return nt == 1 ? 4 : nt == 2 ? 3 : 2; }
 
@@ -243,8 +255,21 @@ AttendPlan plan_attend(const sa_kv4_cache* c, int heads, int T, bool weights) {
     a.off_scores = off;
     if (weights) off += align_up(planes * c->capacity * a.score_rows * sizeof(float), 256);
   } else {
-    a.off_scores = off;
-    off += align_up(static_cast<size_t>(c->batch) * heads * T * sizeof(float), 256);
+    auto take = [&](size_t bytes) {
+      const size_t at = off;
+      off += align_up(bytes, 256);
+      return at;
+    };
+    a.q_tiles = (rows + 127) / 128;
+    a.pairs = (a.q_tiles + 1) / 2;
+    const size_t q_rows = planes * a.q_tiles * 128;
+    a.off_q = take(q_rows * D * 2);
+    a.off_scale = take(q_rows * sizeof(float));
+    a.off_lse = take(q_rows * sizeof(float));
+    a.off_line = take((c->batch + 1) * sizeof(long long));
+    a.off_pre = take(static_cast<size_t>(c->batch) * (a.pairs + 1) * sizeof(int));
+    a.off_o = take(2ull * kMostSms * 256 * D * sizeof(float));
+    a.off_ml = take(2ull * kMostSms * 256 * sizeof(float2));
   }
   a.total = off;
   return a;
@@ -273,6 +298,21 @@ bool launch_decode_nt(const sa::Kv4AttendParams& p, int nt, cudaStream_t s) {
   return nt == 1   ? launch_decode<D, 1, kDtype, false>(p, s)
          : nt == 2 ? launch_decode<D, 2, kDtype, false>(p, s)
                    : launch_decode<D, 4, kDtype, false>(p, s);
+}
+
+template <int D, int kDtype>
+bool launch_chunk(const sa::Kv4AttendParams& p, cudaStream_t s) {
+  using S = sa::ChunkShape<D>;
+  if (!allow_smem<sa::kv4_chunk_kernel<D, kDtype>>(S::kSmem, 128)) return false;
+  const int blocks = std::min(sm_count(), kMostSms);
+  sa::kv4_stage_kernel<D, kDtype><<<dim3(p.q_tiles + 1, p.c.H, p.c.B), 256, 0, s>>>(p);
+  launch_after(sa::kv4_chunk_kernel<D, kDtype>, dim3(blocks), dim3(S::kThreads), S::kSmem, s, p);
+  if (blocks > 1)
+    launch_after(sa::kv4_chunk_join_kernel<D, kDtype>, dim3(blocks - 1, 8), dim3(128), 0, s, p,
+                 blocks);
+  if (p.add_weight)
+    sa::kv4_weight_rows_kernel<D, kDtype><<<dim3(p.c.N / 128, p.c.H, p.c.B), 128, 0, s>>>(p);
+  return true;
 }
 
 size_t evict_bytes(const sa_kv4_cache* c) {
@@ -407,21 +447,18 @@ SA_API int sa_kv4_attend(const sa_kv4_cache* c, const sa_rows* Q, const sa_rows*
     if (!ok) return refuse(SA_ERR_CUDA, "shared memory of the attention kernel");
     return launched("attention");
   }
-  const dim3 grid((T + 3) / 4, heads, p.c.B), wgrid(p.c.N / 128, p.c.H, p.c.B);
-  auto run = [&](auto attend, auto weights) {
-    attend<<<grid, 128, 0, s>>>(p);
-    if (add_weight) weights<<<wgrid, 128, 0, s>>>(p);
-  };
-  if (D == 128)
-    dtype == SA_DTYPE_FP16 ? run(sa::kv4_attend_rows_kernel<128, SA_DTYPE_FP16>,
-                                 sa::kv4_weight_rows_kernel<128, SA_DTYPE_FP16>)
-                           : run(sa::kv4_attend_rows_kernel<128, SA_DTYPE_BF16>,
-                                 sa::kv4_weight_rows_kernel<128, SA_DTYPE_BF16>);
-  else
-    dtype == SA_DTYPE_FP16 ? run(sa::kv4_attend_rows_kernel<64, SA_DTYPE_FP16>,
-                                 sa::kv4_weight_rows_kernel<64, SA_DTYPE_FP16>)
-                           : run(sa::kv4_attend_rows_kernel<64, SA_DTYPE_BF16>,
-                                 sa::kv4_weight_rows_kernel<64, SA_DTYPE_BF16>);
+  p.q_tiles = plan.q_tiles;
+  p.pairs = plan.pairs;
+  p.q_img = ws + plan.off_q;
+  p.row_scale = reinterpret_cast<float*>(ws + plan.off_scale);
+  p.row_lse = reinterpret_cast<float*>(ws + plan.off_lse);
+  p.line = reinterpret_cast<long long*>(ws + plan.off_line);
+  p.pre = reinterpret_cast<int*>(ws + plan.off_pre);
+  const bool ok = D == 128 ? (dtype == SA_DTYPE_FP16 ? launch_chunk<128, SA_DTYPE_FP16>(p, s)
+                                                     : launch_chunk<128, SA_DTYPE_BF16>(p, s))
+                           : (dtype == SA_DTYPE_FP16 ? launch_chunk<64, SA_DTYPE_FP16>(p, s)
+                                                     : launch_chunk<64, SA_DTYPE_BF16>(p, s));
+  if (!ok) return refuse(SA_ERR_CUDA, "resources of the attention kernel");
   return launched("attention");
 }
 
