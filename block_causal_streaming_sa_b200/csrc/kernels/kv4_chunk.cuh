@@ -75,51 +75,39 @@ __device__ __forceinline__ int pair_tiles(const Kv4AttendParams& p, int held, in
   return (rows_seen(p, held, n_tok, last / p.group) + 127) / 128;
 }
 
-// Queries to fp16 tiles, per-row scales, and the schedule. Block (x, h, b) stages
-// tile x; block (n_tiles, 0, 0) sums up the steps: line[b] = steps before sequence b,
-// pre[b][pair] = steps of one head of b before that pair (last entry: of all pairs).
+// Query tiles that draw weight from key tile `kt`: from the tile of the first token
+// that sees one of its rows on. `from` is that tile.
+__device__ __forceinline__ int weight_steps(const Kv4AttendParams& p, int held, int n_tok, int kt,
+                                            int& from) {
+  from = 0;
+  if (kt * 128 >= held) return 0;
+  const int tiles = (n_tok * p.group + 127) / 128;
+  if (p.causal) from = max(kt * 128 - (held - n_tok), 0) * p.group / 128;
+  return max(tiles - from, 0);
+}
+
+// Queries to fp16 tiles, per-row scales, and the lines of steps. Block (x, h, b)
+// stages tile x; blocks (q_tiles, 0, 0) and (q_tiles + 1, 0, 0) lay the lines.
 template <int D, int kDtype>
 __global__ void __launch_bounds__(256)
     kv4_stage_kernel(const __grid_constant__ Kv4AttendParams p) {
   constexpr int C = D / 8;  // 16-byte pieces of a row
   const Kv4& c = p.c;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (static_cast<int>(blockIdx.x) == p.q_tiles) {
+  if (static_cast<int>(blockIdx.x) >= p.q_tiles) {
     if (blockIdx.y != 0 || blockIdx.z != 0) return;
-    __shared__ int warp_sum[8];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    long long before = 0;
-    for (int b = 0; b < c.B; ++b) {
-      const int held = rows_held(c, b), n_tok = tokens_of(p.counts, b, p.T);
-      if (threadIdx.x == 0) check_order(p, b, n_tok);
-      int sum = 0;
-      int* pre = p.pre + static_cast<size_t>(b) * (p.pairs + 1);
-      for (int q0 = 0; q0 < p.pairs; q0 += 256) {
-        const int q = q0 + threadIdx.x;
-        const int v = q < p.pairs ? pair_tiles(p, held, n_tok, q) : 0;
-        int x = v;
-#pragma unroll
-        for (int k = 1; k < 32; k <<= 1) {
-          const int y = __shfl_up_sync(~0u, x, k);
-          if (lane >= k) x += y;
-        }
-        if (lane == 31) warp_sum[warp] = x;
-        __syncthreads();
-        int base = sum;
-        for (int w = 0; w < 8; ++w) {
-          if (w < warp) base += warp_sum[w];
-          sum += warp_sum[w];
-        }
-        if (q < p.pairs) pre[q] = base + x - v;
-        __syncthreads();
-      }
-      if (threadIdx.x == 0) {
-        pre[p.pairs] = sum;
-        p.line[b] = before;
-      }
-      before += static_cast<long long>(sum) * c.H;
+    if (static_cast<int>(blockIdx.x) == p.q_tiles) {
+      lay_line(p.line, c.B, c.H, [&](int b, int i) {
+        const int n_tok = tokens_of(p.counts, b, p.T);
+        if (i == 0) check_order(p, b, n_tok);
+        return pair_tiles(p, rows_held(c, b), n_tok, i);
+      });
+    } else {
+      lay_line(p.weight_line, c.B, c.H, [&](int b, int i) {
+        int from;
+        return weight_steps(p, rows_held(c, b), tokens_of(p.counts, b, p.T), i, from);
+      });
     }
-    if (threadIdx.x == 0) p.line[c.B] = before;
     return;
   }
   const int b = blockIdx.z, h = blockIdx.y, tile = blockIdx.x;
@@ -151,65 +139,17 @@ __global__ void __launch_bounds__(256)
     *reinterpret_cast<uint4*>(dst + tile_offset(r, piece)) = make_uint4(x[0], x[1], x[2], x[3]);
     if (piece == 0) p.row_scale[tile_id * 128 + r] = row < n_rows ? p.scale_log2 / f : 0.f;
     if (row >= n_rows) {
-      if (piece == 0) p.row_lse[tile_id * 128 + r] = INFINITY;  // such rows draw no weight
+      if (piece == 0) p.row_nlse[tile_id * 128 + r] = -INFINITY;  // such rows draw no weight
     } else if (empty) {
       uint16_t* o = static_cast<uint16_t*>(p.o.data) + b * p.o.sb + t * p.o.st + hq * p.o.sh;
       *reinterpret_cast<uint4*>(o + piece * 8) = make_uint4(0u, 0u, 0u, 0u);
       if (piece == 0) {
         if (p.lse != nullptr)
           p.lse[(static_cast<size_t>(b) * p.heads + hq) * p.T + t] = -INFINITY;
-        p.row_lse[tile_id * 128 + r] = INFINITY;
+        p.row_nlse[tile_id * 128 + r] = -INFINITY;
       }
     }
   }
-}
-
-// A walk along the line of steps: the pairs of a range, each with its key tiles.
-struct ChunkWalk {
-  long long at, stop;  // steps of the line
-  int b, h, pair;
-  int t0, t1, n;  // key tiles [t0, t1) of n
-
-  __device__ __forceinline__ void start(const Kv4AttendParams& p, long long from, long long to) {
-    at = from;
-    stop = to;
-    b = h = pair = t0 = t1 = n = 0;
-  }
-  // The next pair of the range; false at its end.
-  __device__ __forceinline__ bool next(const Kv4AttendParams& p) {
-    if (at >= stop) return false;
-    while (at >= p.line[b + 1]) ++b;
-    const int* pre = p.pre + static_cast<size_t>(b) * (p.pairs + 1);
-    const int per_head = pre[p.pairs];
-    const long long in_b = at - p.line[b];
-    h = static_cast<int>(in_b / per_head);
-    const int in_h = static_cast<int>(in_b % per_head);
-    int lo = 0, hi = p.pairs;  // pre[lo] <= in_h < pre[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (pre[mid] <= in_h)
-        lo = mid;
-      else
-        hi = mid;
-    }
-    // of pairs without steps that share a start, the last is the one with steps
-    pair = lo;
-    n = pre[pair + 1] - pre[pair];
-    t0 = in_h - pre[pair];
-    t1 = static_cast<int>(min(static_cast<long long>(n), t0 + (stop - at)));
-    at += t1 - t0;
-    return true;
-  }
-};
-
-__device__ __forceinline__ long long chunk_share(const Kv4AttendParams& p, int blocks) {
-  return (p.line[p.c.B] + blocks - 1) / blocks;
-}
-
-// Where a block leaves the partial result of a pair: a range that begins inside a
-// pair (t0 > 0) can do so once, a range that ends inside one it began (t0 = 0) too.
-__device__ __forceinline__ size_t partial_slot(int block, int t0) {
-  return 2 * static_cast<size_t>(block) + (t0 > 0 ? 0 : 1);
 }
 
 // One query row's result: O / l to its place, or the partial row. A function of its
@@ -255,8 +195,8 @@ __device__ __noinline__ void chunk_epilogue(const Kv4AttendParams& p, uint32_t t
     const float lse2 = lsum == 0.f ? -INFINITY : m + log2f(lsum);
     if (p.lse != nullptr)
       p.lse[(static_cast<size_t>(b) * p.heads + hq) * p.T + t] = lse2 * 0.69314718055994531f;
-    p.row_lse[((static_cast<size_t>(b) * p.c.H + h) * p.q_tiles) * 128 + row] =
-        lsum == 0.f ? INFINITY : lse2;
+    p.row_nlse[((static_cast<size_t>(b) * p.c.H + h) * p.q_tiles) * 128 + row] =
+        lsum == 0.f ? -INFINITY : -lse2;
   }
 }
 
@@ -344,9 +284,7 @@ __global__ void __launch_bounds__(512, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
   asm volatile("griddepcontrol.wait;" ::: "memory");  // staged queries and schedule
 
-  const long long share = chunk_share(p, gridDim.x);
-  ChunkWalk walk;
-  walk.start(p, min(blockIdx.x * share, p.line[c.B]), min((blockIdx.x + 1) * share, p.line[c.B]));
+  LineWalk walk = line_range(p.line, c.B);
 
   if (warp >= 12) {
     ptx::setmaxnreg_dec<S::kRegsIssue>();
@@ -384,11 +322,11 @@ __global__ void __launch_bounds__(512, 1)
                        ptx::smem_desc_sw128(vb + kk * 16 * 128, S::kBox, 1024), S::kIdescPV,
                        (accumulate || kk > 0) ? 1u : 0u);
       };
-      while (ok && walk.next(p)) {
+      while (ok && walk.next(p.line)) {
         const int n_rows = tokens_of(p.counts, walk.b, p.T) * p.group;
-        const int tiles = n_rows > walk.pair * 256 + 128 ? 2 : 1;
+        const int tiles = n_rows > walk.item * 256 + 128 ? 2 : 1;
         const size_t tile_id =
-            (static_cast<size_t>(walk.b) * c.H + walk.h) * p.q_tiles + 2 * walk.pair;
+            (static_cast<size_t>(walk.b) * c.H + walk.h) * p.q_tiles + 2 * walk.item;
         for (int i = 0; i < tiles && ok; ++i) {
           // every product that read the previous tile is done once its O is final
           if (q_units[i] > 0)
@@ -469,7 +407,7 @@ __global__ void __launch_bounds__(512, 1)
         phase ^= 1u;
       }
     };
-    while (ok && walk.next(p)) {
+    while (ok && walk.next(p.line)) {
       const int held = rows_held(c, walk.b);
       const size_t plane = (static_cast<size_t>(walk.b) * c.H + walk.h) * c.N;
       ConvertRegs<D> kx, vx;
@@ -495,11 +433,11 @@ __global__ void __launch_bounds__(512, 1)
     const uint32_t tO = tmem + t_lane + S::col_o(i);
     uint32_t s_phase = 0, units = 0;
     bool ok = true;
-    while (ok && walk.next(p)) {
+    while (ok && walk.next(p.line)) {
       const int held = rows_held(c, walk.b), n_tok = tokens_of(p.counts, walk.b, p.T);
       const int n_rows = n_tok * p.group;
-      if (i == 1 && n_rows <= walk.pair * 256 + 128) continue;
-      const int row = walk.pair * 256 + i * 128 + r;
+      if (i == 1 && n_rows <= walk.item * 256 + 128) continue;
+      const int row = walk.item * 256 + i * 128 + r;
       const int end = row < n_rows ? rows_seen(p, held, n_tok, row / p.group) : held;
       const float sl =
           p.row_scale[((static_cast<size_t>(walk.b) * c.H + walk.h) * p.q_tiles) * 128 + row];
@@ -598,41 +536,31 @@ __global__ void __launch_bounds__(512, 1)
   if (warp == 12) ptx::tmem_dealloc(tmem, S::kTmemCols);
 }
 
-// Merge of the pairs that lie in several blocks' ranges: block x takes the pair in
-// which range x begins, if it begins inside one and no earlier range does. A thread
-// per query row, 32 rows (blockIdx.y) of the pair's 256.
+// Merge of the pairs that lie in several blocks' ranges, one boundary (blockIdx.x) and 32
+// of the 256 query rows (blockIdx.y) a block.
 template <int D, int kDtype>
 __global__ void __launch_bounds__(128)
     kv4_chunk_join_kernel(const __grid_constant__ Kv4AttendParams p, int blocks) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Kv4& c = p.c;
-  const long long share = chunk_share(p, blocks), total = p.line[c.B];
-  const long long from = (blockIdx.x + 1) * share;
-  if (from >= total) return;
-  ChunkWalk w;
-  w.start(p, from, total);
-  w.next(p);
-  const long long begin = from - w.t0, end = begin + w.n;  // the pair's steps
-  if (w.t0 == 0 || from - share > begin) return;  // not split here, or an earlier block's
-  const int first = static_cast<int>(begin / share), last = static_cast<int>((end - 1) / share);
+  SplitItem split;
+  if (!split.find(p.line, c.B, blocks, blockIdx.x)) return;
+  const LineWalk& w = split.w;
   const int n_tok = tokens_of(p.counts, w.b, p.T), n_rows = n_tok * p.group;
   // four threads a row, D / 4 values each: r = row in the pair
   const int r = blockIdx.y * 32 + (threadIdx.x & 31), part = threadIdx.x >> 5;
-  const int row = w.pair * 256 + r;
+  const int row = w.item * 256 + r;
   if (row >= n_rows) return;
-  auto slot_of = [&](int block) {
-    return partial_slot(block, block == first && first * share <= begin ? 0 : 1);
-  };
   float mx = -INFINITY;
-  for (int k = first; k <= last; ++k) mx = fmaxf(mx, p.part_ml[slot_of(k) * 256 + r].x);
+  for (int k = split.first; k <= split.last; ++k) mx = fmaxf(mx, p.part_ml[split.slot(k) * 256 + r].x);
   const float ref = mx == -INFINITY ? 0.f : mx;
   float sum = 0.f;
   constexpr int V = D / 16;  // float4 of a thread
   float4 acc[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k = first; k <= last; ++k) {
-    const size_t slot = slot_of(k);
+  for (int k = split.first; k <= split.last; ++k) {
+    const size_t slot = split.slot(k);
     const float2 ml = p.part_ml[slot * 256 + r];
     const float a = ptx::ex2(ml.x - ref);
     sum += ml.y * a;
@@ -662,8 +590,8 @@ __global__ void __launch_bounds__(128)
     const float lse2 = sum == 0.f ? -INFINITY : mx + log2f(sum);
     if (p.lse != nullptr)
       p.lse[(static_cast<size_t>(w.b) * p.heads + hq) * p.T + t] = lse2 * 0.69314718055994531f;
-    p.row_lse[((static_cast<size_t>(w.b) * c.H + w.h) * p.q_tiles) * 128 + row] =
-        sum == 0.f ? INFINITY : lse2;
+    p.row_nlse[((static_cast<size_t>(w.b) * c.H + w.h) * p.q_tiles) * 128 + row] =
+        sum == 0.f ? -INFINITY : -lse2;
   }
 }
 

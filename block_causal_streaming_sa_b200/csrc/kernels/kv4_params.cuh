@@ -6,6 +6,15 @@
 
 namespace sa {
 
+// Work of many unequal items laid out as one line of steps and cut into equal ranges,
+// one a block: sequence by sequence, KV head by KV head, item by item. Heads of a
+// sequence have the same items.
+struct StepLine {
+  long long* begin;  // [B + 1]: steps before sequence b
+  int* pre;          // [B][items + 1]: steps of one head of b before that item
+  int items;
+};
+
 // Query rows of one (sequence, KV head): row r is token r / group, query head
 // h * group + r % group. Rows of one token are neighbours, so a tile of rows spans
 // few tokens and, under a causal mask, ends early.
@@ -22,13 +31,14 @@ struct Kv4AttendParams {
   float2* part_ml; // [slot][rows of a block]: maximum (base 2), sum
   float* scores;   // [B][H][N][score_rows], base 2
   int score_rows;
-  // many query rows (kv4_chunk.cuh)
-  int q_tiles, pairs;  // tiles of 128 query rows per (sequence, KV head), and pairs of them
-  uint8_t* q_img;      // [B][H][q_tiles] shared memory images of the fp16 query tiles
-  float* row_scale;    // [B][H][q_tiles * 128]: score factor of a staged row
-  float* row_lse;      // the same: base-2 log-sum-exp, +inf where no weight is drawn
-  long long* line;     // [B + 1]
-  int* pre;            // [B][pairs + 1]
+  // many query rows (kv4_chunk.cuh, kv4_weights.cuh)
+  int q_tiles, pairs;    // tiles of 128 query rows per (sequence, KV head), and pairs of them
+  uint8_t* q_img;        // [B][H][q_tiles] shared memory images of the fp16 query tiles
+  float* row_scale;      // [B][H][q_tiles * 128]: score factor of a staged row
+  float* row_nlse;       // the same: minus its base-2 log-sum-exp, -inf if it draws no weight
+  StepLine line;         // steps of the attention: pairs x key tiles
+  StepLine weight_line;  // steps of the weights: key tiles x query tiles
+  float* part_w;         // [slot][128]: partial sums of weights
 };
 
 // Rows that query token t of sequence b reads.
@@ -51,5 +61,125 @@ __device__ __forceinline__ float row_factor(float amax) {
   if (!(amax > 0.f) || e >= 255u) return 1.f;
   return __uint_as_float((254u - min(max(e, 1u), 253u)) << 23);
 }
+
+// Fills `line` from tiles(b, item), the steps of an item: one block of 256 threads, a
+// sequence per warp.
+template <typename F>
+__device__ __forceinline__ void lay_line(const StepLine& line, int B, int H, F tiles) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int b = warp; b < B; b += 8) {
+    int* pre = line.pre + static_cast<size_t>(b) * (line.items + 1);
+    int sum = 0;
+    for (int i0 = 0; i0 < line.items; i0 += 32) {
+      const int v = i0 + lane < line.items ? tiles(b, i0 + lane) : 0;
+      int x = v;
+#pragma unroll
+      for (int k = 1; k < 32; k <<= 1) {
+        const int y = __shfl_up_sync(~0u, x, k);
+        if (lane >= k) x += y;
+      }
+      if (i0 + lane < line.items) pre[i0 + lane] = sum + x - v;
+      sum += __shfl_sync(~0u, x, 31);
+    }
+    if (lane == 0) {
+      pre[line.items] = sum;
+      line.begin[b + 1] = static_cast<long long>(sum) * H;
+    }
+  }
+  __syncthreads();
+  if (warp == 0) {
+    if (lane == 0) line.begin[0] = 0;
+    long long sum = 0;
+    for (int b0 = 0; b0 < B; b0 += 32) {
+      long long x = b0 + lane < B ? line.begin[b0 + lane + 1] : 0;
+#pragma unroll
+      for (int k = 1; k < 32; k <<= 1) {
+        const long long y = __shfl_up_sync(~0u, x, k);
+        if (lane >= k) x += y;
+      }
+      if (b0 + lane < B) line.begin[b0 + lane + 1] = sum + x;
+      sum += __shfl_sync(~0u, x, 31);
+    }
+  }
+}
+
+// A walk along a range of a line: its items, each with its steps [t0, t1) of n.
+struct LineWalk {
+  long long at, stop;
+  int b, h, item;
+  int t0, t1, n;
+
+  __device__ __forceinline__ void start(long long from, long long to) {
+    at = from;
+    stop = to;
+    b = h = item = t0 = t1 = n = 0;
+  }
+  // The next item of the range; false at its end.
+  __device__ __forceinline__ bool next(const StepLine& line) {
+    if (at >= stop) return false;
+    while (at >= line.begin[b + 1]) ++b;
+    const int* pre = line.pre + static_cast<size_t>(b) * (line.items + 1);
+    const int per_head = pre[line.items];
+    const long long in_b = at - line.begin[b];
+    h = static_cast<int>(in_b / per_head);
+    const int in_h = static_cast<int>(in_b % per_head);
+    int lo = 0, hi = line.items;  // pre[lo] <= in_h < pre[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (pre[mid] <= in_h)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    // of items without steps that share a start, the last is the one with steps
+    item = lo;
+    n = pre[item + 1] - pre[item];
+    t0 = in_h - pre[item];
+    t1 = static_cast<int>(min(static_cast<long long>(n), t0 + (stop - at)));
+    at += t1 - t0;
+    return true;
+  }
+};
+
+__device__ __forceinline__ long long line_share(const StepLine& line, int B, int blocks) {
+  return (line.begin[B] + blocks - 1) / blocks;
+}
+
+// This block's range of the line.
+__device__ __forceinline__ LineWalk line_range(const StepLine& line, int B) {
+  const long long share = line_share(line, B, gridDim.x), total = line.begin[B];
+  LineWalk w;
+  w.start(min(blockIdx.x * share, total), min((blockIdx.x + 1) * share, total));
+  return w;
+}
+
+// Where a block leaves the partial result of an item: a range that begins inside one
+// (t0 > 0) can do so once, a range that ends inside one it began (t0 = 0) too.
+__device__ __forceinline__ size_t partial_slot(int block, int t0) {
+  return 2 * static_cast<size_t>(block) + (t0 > 0 ? 0 : 1);
+}
+
+// An item that lies in several blocks' ranges, found from the one boundary (block
+// ranges `boundary` and `boundary` + 1) that has to merge it: the first inside it.
+struct SplitItem {
+  LineWalk w;
+  int first, last;  // blocks that have a part
+
+  __device__ __forceinline__ bool find(const StepLine& line, int B, int blocks, int boundary) {
+    const long long share = line_share(line, B, blocks), total = line.begin[B];
+    const long long from = (boundary + 1) * share;
+    if (from >= total) return false;
+    w.start(from, total);
+    w.next(line);
+    const long long begin = from - w.t0, end = begin + w.n;
+    if (w.t0 == 0 || from - share > begin) return false;
+    first = static_cast<int>(begin / share);
+    last = static_cast<int>((end - 1) / share);
+    return true;
+  }
+  __device__ __forceinline__ size_t slot(int block) const {
+    return partial_slot(block, block == first ? 0 : 1);
+  }
+};
 
 }  // namespace sa

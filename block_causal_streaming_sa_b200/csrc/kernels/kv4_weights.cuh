@@ -1,0 +1,272 @@
+// Attention weight drawn by the rows of a 4-bit cache from many query rows:
+//   weight[j] += sum over queries l of 2^(s_lj - lse_l)
+// after the attention has left every query's log-sum-exp.
+//
+// One product and one exponential per (query row, cache row), so bound by the
+// exponential unit (128 x 128 of them take twice the cycles of the product).
+// Transposed scores S^T = K Q^T put a cache row on a thread, so its sum stays in the
+// thread's registers over all queries: no reduction across threads and no atomics,
+// the same bits on every run. K is converted once per key tile; query tiles stream
+// past it as bulk copies of the staged images, with the rows' scales and
+// log-sum-exps. Storing the attention's own probabilities instead would move 2 bytes
+// per pair, more than the product costs.
+//
+//  * Steps (key tile, query tile) are cut evenly over the blocks like the attention's.
+//  * warp 13 loads query tiles into a ring of four stages; warp 12 issues the products
+//    into the four tensor memory buffers of the same numbers; warpgroups 0 and 1 take
+//    every other step; warps 8-11 convert key tiles, one ahead.
+#pragma once
+
+#include "kv4_chunk.cuh"
+
+namespace sa {
+
+template <int D>
+struct WeightShape {
+  static constexpr int kTile = 128 * D * 2;
+  static constexpr int kStages = 4;
+  static constexpr int kThreads = 448;
+  static constexpr int kOffK = 0;                              // two key tiles
+  static constexpr int kOffQ = 2 * kTile;                      // query tiles
+  static constexpr int kOffRow = kOffQ + kStages * kTile;      // [stage][scale | -lse][128]
+  static constexpr int kOffAcc = kOffRow + kStages * 1024;     // [2][128]
+  static constexpr int kOffBar = kOffAcc + 1024;
+  static constexpr int kSmem = kOffBar + 256 + 1024;           // + alignment slack
+  static constexpr uint32_t kIdesc = ptx::idesc_f32acc(128, 128, 0, 0);
+  __host__ __device__ static constexpr int QFULL(int s) { return s; }
+  __host__ __device__ static constexpr int SFULL(int s) { return kStages + s; }
+  __host__ __device__ static constexpr int EMPTY(int s) { return 2 * kStages + s; }
+  __host__ __device__ static constexpr int KFULL(int i) { return 3 * kStages + i; }
+  __host__ __device__ static constexpr int KEMPTY(int i) { return 3 * kStages + 2 + i; }
+  __host__ __device__ static constexpr int DRAIN() { return 3 * kStages + 4; }
+  static_assert(kSmem <= 232448, "shared memory");
+};
+
+template <int D>
+__global__ void __launch_bounds__(448, 1)
+    kv4_weight_kernel(const __grid_constant__ Kv4AttendParams p) {
+  using S = WeightShape<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const Kv4& c = p.c;
+  const uint32_t raw = ptx::smem_addr(smem_raw);
+  uint8_t* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+  const uint32_t sbase = ptx::smem_addr(smem);
+  auto bar = [&](int i) { return sbase + S::kOffBar + 8u * static_cast<uint32_t>(i); };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kOffBar + 240);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kOffBar + 248);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::kStages; ++s) {
+      ptx::mbar_init(bar(S::QFULL(s)), 1);
+      ptx::mbar_init(bar(S::SFULL(s)), 1);
+      ptx::mbar_init(bar(S::EMPTY(s)), 4);  // the four warps that read the step
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(bar(S::KFULL(i)), 4);  // the four converting warps
+      ptx::mbar_init(bar(S::KEMPTY(i)), 1);
+    }
+    ptx::mbar_init(bar(S::DRAIN()), 1);
+    *abort_flag = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 12) {
+    ptx::tmem_alloc(ptx::smem_addr(tmem_slot), 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the attention's log-sum-exps
+
+  LineWalk walk = line_range(p.weight_line, c.B);
+  auto wait = [&](int which, uint32_t parity) {
+    return ptx::mbar_wait(bar(which), parity, abort_flag, c.status);
+  };
+  // Query tile of step t of the walk's item.
+  auto first_tile = [&]() {
+    int from;
+    weight_steps(p, rows_held(c, walk.b), tokens_of(p.counts, walk.b, p.T), walk.item, from);
+    return from + walk.t0;
+  };
+
+  if (warp == 13) {
+    // -------------------------------------------------------------- query tiles
+    if (lane == 0) {
+      uint32_t step = 0;
+      bool ok = true;
+      while (ok && walk.next(p.weight_line)) {
+        const size_t tile0 = (static_cast<size_t>(walk.b) * c.H + walk.h) * p.q_tiles + first_tile();
+        for (int t = 0; t < walk.t1 - walk.t0; ++t, ++step) {
+          const int s = step % S::kStages;
+          ok = wait(S::EMPTY(s), ((step / S::kStages) & 1) ^ 1u);
+          if (!ok) break;
+          const uint32_t full = bar(S::QFULL(s)), row = sbase + S::kOffRow + s * 1024;
+          ptx::mbar_arrive_expect_tx(full, S::kTile + 1024);
+          auto load = [&](uint32_t dst, const void* src, uint32_t bytes) {
+            asm volatile(
+                "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], "
+                "%2, [%3];" ::"r"(dst),
+                "l"(src), "r"(bytes), "r"(full)
+                : "memory");
+          };
+          load(sbase + S::kOffQ + s * S::kTile, p.q_img + (tile0 + t) * S::kTile, S::kTile);
+          load(row, p.row_scale + (tile0 + t) * 128, 512);
+          load(row + 512, p.row_nlse + (tile0 + t) * 128, 512);
+        }
+      }
+      // copies under way land before the block can end
+      volatile int none = 0;
+      for (uint32_t k = step > S::kStages ? step - S::kStages : 0; k < step; ++k)
+        ptx::mbar_wait(bar(S::QFULL(k % S::kStages)), (k / S::kStages) & 1, &none, c.status);
+    }
+  } else if (warp == 12) {
+    // -------------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      uint32_t step = 0, unit = 0;
+      bool ok = true;
+      while (ok && walk.next(p.weight_line)) {
+        const int kb = unit & 1;
+        ok = wait(S::KFULL(kb), (unit >> 1) & 1);
+        for (int t = walk.t0; ok && t < walk.t1; ++t, ++step) {
+          const int s = step % S::kStages;
+          ok = wait(S::QFULL(s), (step / S::kStages) & 1);
+          if (!ok) break;
+          ptx::tc_fence_after();
+          const uint32_t ka = sbase + S::kOffK + kb * S::kTile;
+          const uint32_t qb = sbase + S::kOffQ + s * S::kTile;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * (128 * 128) + (kk & 3) * 32;
+            ptx::umma_ss(tmem + s * 128, ptx::smem_desc_sw128(ka + off, 16, 1024),
+                         ptx::smem_desc_sw128(qb + off, 16, 1024), S::kIdesc, kk > 0 ? 1u : 0u);
+          }
+          ptx::umma_commit(bar(S::SFULL(s)));
+        }
+        if (ok) ptx::umma_commit(bar(S::KEMPTY(kb)));
+        ++unit;
+      }
+      volatile int none = 0;
+      ptx::umma_commit(bar(S::DRAIN()));
+      ptx::mbar_wait(bar(S::DRAIN()), 0, &none, c.status);
+    }
+  } else if (warp >= 8) {
+    // -------------------------------------------------------------- conversion
+    const int tid = threadIdx.x - 256;
+    uint32_t unit = 0;
+    while (walk.next(p.weight_line)) {
+      const int kb = unit & 1;
+      const size_t row0 = (static_cast<size_t>(walk.b) * c.H + walk.h) * c.N +
+                          static_cast<size_t>(walk.item) * 128;
+      ConvertRegs<D> x;
+      convert_load<D>(x, c.k_codes, c.k_scales, row0, tid);
+      if (!__all_sync(~0u, wait(S::KEMPTY(kb), ((unit >> 1) & 1) ^ 1u))) break;
+      convert_store<D>(x, sbase + S::kOffK + kb * S::kTile, tid,
+                       rows_held(c, walk.b) - walk.item * 128);
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar(S::KFULL(kb)));
+      ++unit;
+    }
+  } else {
+    // -------------------------------------------------------------- sums
+    const int wg = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    float* s_acc = reinterpret_cast<float*>(smem + S::kOffAcc);
+    uint32_t step = 0, unit = 0;
+    bool ok = true;
+    while (walk.next(p.weight_line)) {
+      const int held = rows_held(c, walk.b), n_tok = tokens_of(p.counts, walk.b, p.T);
+      const int j = walk.item * 128 + r;
+      // first query row that sees row j
+      const int row_min = p.causal ? max(j - (held - n_tok), 0) * p.group : 0;
+      const int tile0 = first_tile();
+      float acc[8];
+#pragma unroll
+      for (int a = 0; a < 8; ++a) acc[a] = 0.f;
+      for (int t = 0; t < walk.t1 - walk.t0; ++t, ++step) {
+        if ((step & 1) != static_cast<uint32_t>(wg)) continue;
+        const int s = step % S::kStages;
+        ok = ok && __all_sync(~0u, wait(S::SFULL(s), (step / S::kStages) & 1));
+        if (!ok) continue;  // the barrier below is still met
+        ptx::tc_fence_after();
+        const int hidden = row_min - (tile0 + t) * 128;  // columns before this see nothing
+        const float* scale = reinterpret_cast<const float*>(smem + S::kOffRow + s * 1024);
+        uint32_t x[2][32];
+        ptx::tmem_ld32(t_lane + s * 128, x[0]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          ptx::tmem_wait_ld();
+          if (q < 3) ptx::tmem_ld32(t_lane + s * 128 + (q + 1) * 32, x[(q + 1) & 1]);
+#pragma unroll
+          for (int k = 0; k < 32; k += 4) {
+            const float4 sl = *reinterpret_cast<const float4*>(scale + q * 32 + k);
+            const float4 nl = *reinterpret_cast<const float4*>(scale + 128 + q * 32 + k);
+            const uint32_t* v = x[q & 1] + k;
+            float e0, e1, e2, e3;
+            ptx::ffma2(e0, e1, __uint_as_float(v[0]), __uint_as_float(v[1]), sl.x, sl.y, nl.x,
+                       nl.y);
+            ptx::ffma2(e2, e3, __uint_as_float(v[2]), __uint_as_float(v[3]), sl.z, sl.w, nl.z,
+                       nl.w);
+            e0 = ptx::ex2(e0);
+            e1 = ptx::ex2(e1);
+            e2 = ptx::ex2(e2);
+            e3 = ptx::ex2(e3);
+            if (hidden > 0) {
+              const int col = q * 32 + k;
+              e0 = col < hidden ? 0.f : e0;
+              e1 = col + 1 < hidden ? 0.f : e1;
+              e2 = col + 2 < hidden ? 0.f : e2;
+              e3 = col + 3 < hidden ? 0.f : e3;
+            }
+            const int a = (k & 4);
+            ptx::fadd2(acc[a], acc[a + 1], acc[a], acc[a + 1], e0, e1);
+            ptx::fadd2(acc[a + 2], acc[a + 3], acc[a + 2], acc[a + 3], e2, e3);
+          }
+        }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(S::EMPTY(s)));
+      }
+      const float sum = ((acc[0] + acc[1]) + (acc[2] + acc[3])) +
+                        ((acc[4] + acc[5]) + (acc[6] + acc[7]));
+      // the two warpgroups' sums, always in the same order
+      if (wg == 1) s_acc[(unit & 1) * 128 + r] = sum;
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (wg == 0 && ok) {
+        const float both = sum + s_acc[(unit & 1) * 128 + r];
+        if (walk.t0 > 0 || walk.t1 < walk.n) {
+          p.part_w[partial_slot(blockIdx.x, walk.t0) * 128 + r] = both;
+        } else if (j < held) {
+          float* w = c.weight + (static_cast<size_t>(walk.b) * c.H + walk.h) * c.N + j;
+          *w += both;
+        }
+      }
+      ++unit;
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  if (warp == 12) ptx::tmem_dealloc(tmem, 512);
+}
+
+// Weights of key tiles that lie in several blocks' ranges, summed in their order.
+__global__ void __launch_bounds__(128)
+    kv4_weight_join_kernel(const __grid_constant__ Kv4AttendParams p, int blocks) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Kv4& c = p.c;
+  SplitItem split;
+  if (!split.find(p.weight_line, c.B, blocks, blockIdx.x)) return;
+  const LineWalk& w = split.w;
+  const int j = w.item * 128 + threadIdx.x;
+  if (j >= rows_held(c, w.b)) return;
+  float sum = 0.f;
+  for (int k = split.first; k <= split.last; ++k)
+    sum += p.part_w[split.slot(k) * 128 + threadIdx.x];
+  c.weight[(static_cast<size_t>(w.b) * c.H + w.h) * c.N + j] += sum;
+}
+
+}  // namespace sa

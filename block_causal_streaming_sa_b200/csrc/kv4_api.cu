@@ -9,11 +9,11 @@
 #include <string>
 
 #include "host_common.h"
-#include "kernels/kv4_attend_rows.cuh"
 #include "kernels/kv4_chunk.cuh"
 #include "kernels/kv4_decode.cuh"
 #include "kernels/kv4_evict.cuh"
 #include "kernels/kv4_rows.cuh"
+#include "kernels/kv4_weights.cuh"
 
 using sa::aligned16;
 using sa::device_memory;
@@ -227,7 +227,7 @@ struct AttendPlan {
   size_t off_o, off_ml, off_scores;
   // many query rows: kv4_chunk.cuh
   int q_tiles, pairs;
-  size_t off_q, off_scale, off_lse, off_line, off_pre;
+  size_t off_q, off_scale, off_nlse, off_begin[2], off_pre[2], off_w;
   size_t total;
 };
 
@@ -265,9 +265,13 @@ AttendPlan plan_attend(const sa_kv4_cache* c, int heads, int T, bool weights) {
     const size_t q_rows = planes * a.q_tiles * 128;
     a.off_q = take(q_rows * D * 2);
     a.off_scale = take(q_rows * sizeof(float));
-    a.off_lse = take(q_rows * sizeof(float));
-    a.off_line = take((c->batch + 1) * sizeof(long long));
-    a.off_pre = take(static_cast<size_t>(c->batch) * (a.pairs + 1) * sizeof(int));
+    a.off_nlse = take(q_rows * sizeof(float));
+    const int items[2] = {a.pairs, c->capacity / 128};
+    for (int i = 0; i < (weights ? 2 : 1); ++i) {
+      a.off_begin[i] = take((c->batch + 1) * sizeof(long long));
+      a.off_pre[i] = take(static_cast<size_t>(c->batch) * (items[i] + 1) * sizeof(int));
+    }
+    if (weights) a.off_w = take(2ull * kMostSms * 128 * sizeof(float));
     a.off_o = take(2ull * kMostSms * 256 * D * sizeof(float));
     a.off_ml = take(2ull * kMostSms * 256 * sizeof(float2));
   }
@@ -305,13 +309,18 @@ bool launch_chunk(const sa::Kv4AttendParams& p, cudaStream_t s) {
   using S = sa::ChunkShape<D>;
   if (!allow_smem<sa::kv4_chunk_kernel<D, kDtype>>(S::kSmem, 128)) return false;
   const int blocks = std::min(sm_count(), kMostSms);
-  sa::kv4_stage_kernel<D, kDtype><<<dim3(p.q_tiles + 1, p.c.H, p.c.B), 256, 0, s>>>(p);
+  sa::kv4_stage_kernel<D, kDtype>
+      <<<dim3(p.q_tiles + (p.add_weight ? 2 : 1), p.c.H, p.c.B), 256, 0, s>>>(p);
   launch_after(sa::kv4_chunk_kernel<D, kDtype>, dim3(blocks), dim3(S::kThreads), S::kSmem, s, p);
   if (blocks > 1)
     launch_after(sa::kv4_chunk_join_kernel<D, kDtype>, dim3(blocks - 1, 8), dim3(128), 0, s, p,
                  blocks);
-  if (p.add_weight)
-    sa::kv4_weight_rows_kernel<D, kDtype><<<dim3(p.c.N / 128, p.c.H, p.c.B), 128, 0, s>>>(p);
+  if (!p.add_weight) return true;
+  using W = sa::WeightShape<D>;
+  if (!allow_smem<sa::kv4_weight_kernel<D>>(W::kSmem)) return false;
+  launch_after(sa::kv4_weight_kernel<D>, dim3(blocks), dim3(W::kThreads), W::kSmem, s, p);
+  if (blocks > 1)
+    launch_after(sa::kv4_weight_join_kernel, dim3(blocks - 1), dim3(128), 0, s, p, blocks);
   return true;
 }
 
@@ -451,9 +460,14 @@ SA_API int sa_kv4_attend(const sa_kv4_cache* c, const sa_rows* Q, const sa_rows*
   p.pairs = plan.pairs;
   p.q_img = ws + plan.off_q;
   p.row_scale = reinterpret_cast<float*>(ws + plan.off_scale);
-  p.row_lse = reinterpret_cast<float*>(ws + plan.off_lse);
-  p.line = reinterpret_cast<long long*>(ws + plan.off_line);
-  p.pre = reinterpret_cast<int*>(ws + plan.off_pre);
+  p.row_nlse = reinterpret_cast<float*>(ws + plan.off_nlse);
+  p.part_w = reinterpret_cast<float*>(ws + plan.off_w);
+  auto line = [&](int i, int items) {
+    return sa::StepLine{reinterpret_cast<long long*>(ws + plan.off_begin[i]),
+                        reinterpret_cast<int*>(ws + plan.off_pre[i]), items};
+  };
+  p.line = line(0, plan.pairs);
+  p.weight_line = line(1, p.c.N / 128);
   const bool ok = D == 128 ? (dtype == SA_DTYPE_FP16 ? launch_chunk<128, SA_DTYPE_FP16>(p, s)
                                                      : launch_chunk<128, SA_DTYPE_BF16>(p, s))
                            : (dtype == SA_DTYPE_FP16 ? launch_chunk<64, SA_DTYPE_FP16>(p, s)
