@@ -1,13 +1,26 @@
 // Eviction from a 4-bit cache by accumulated attention weight.
 //
-// Per (sequence, KV head) with more than `keep` rows: the keep-th largest key is
-// found by radix selection over 32-bit ordered keys (four passes of eight bits,
-// histogram in shared memory), then one ordered pass numbers the evicted rows
-// below `keep` (holes) and the kept rows from `keep` on (movers); hole j takes
-// mover j. Only rows that have to move do: one per evicted row at most, instead
-// of a shift of everything behind the first evicted row. Writes go below `keep`,
-// reads come from `keep` on, so the moves need no order among themselves.
+// Reads a weight and a position (8 bytes) a row and moves at most one row per evicted
+// one: kept rows from `keep` on go into the places of evicted rows below it, instead
+// of everything behind the first evicted row moving up. Small next to an attention
+// over the same rows in bytes, so what counts is the chain of dependent steps; all of
+// it is one launch:
+//  * a cluster of 1 to 8 blocks per (sequence, KV head) keeps the rows' keys (ordered
+//    32-bit images of the weights) in shared memory, read once;
+//  * the keep-th largest key by radix selection, 10 + 11 + 11 bits: a histogram a
+//    block, searched over the cluster through distributed shared memory by every block
+//    alike, so a pass costs one cluster barrier. The search goes through sums of 32 or
+//    64 bins first: reading all 2048 bins of 8 blocks took 12 K cycles a pass, the two
+//    steps 2 K. In the first pass weights crowd into a few exponents: neighbouring
+//    lanes count in eight copies (one copy: 6 K cycles for 4096 rows);
+//  * rows are numbered in order: each warp owns consecutive rows and counts, by
+//    ballots, those above and equal to that key on both sides of `keep`; two scans over
+//    the warps and arithmetic give the places of its holes and movers;
+//  * the j-th hole takes the j-th mover. Writes go below `keep`, reads come from `keep`
+//    on, so the moves need no order among themselves.
 #pragma once
+
+#include <cooperative_groups.h>
 
 #include "kv4_format.cuh"
 
@@ -16,9 +29,13 @@ namespace sa {
 struct Kv4EvictParams {
   Kv4 c;
   int keep, first, recent;
-  int32_t* n_moves;  // [B][H]
-  int32_t* lists;    // [B][H][N]: holes from the front, movers from N / 2
+  int smem_keys;   // keys a block keeps in shared memory; rows beyond are read again
+  int32_t* lists;  // [B][H][N]: holes from the front, movers from N / 2
 };
+
+constexpr int kEvictCopies = 8;
+constexpr int kEvictHist = (kEvictCopies + 1) * 1024 + 2 * 2048;
+constexpr int kEvictFixedSmem = (kEvictHist + 96 + 64) * 4 + 2 * 32 * 8;
 
 // Order of a row among its head's: protected rows above every weight, NaN below,
 // equal numbers (both zeros among them) equal.
@@ -29,130 +46,263 @@ __device__ __forceinline__ unsigned evict_key(float w, int pos, int first, int k
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(1024) kv4_evict_select_kernel(
-    const __grid_constant__ Kv4EvictParams p) {
-  const Kv4& c = p.c;
-  const int h = blockIdx.x, b = blockIdx.y;
-  const int n = rows_held(c, b);
-  const size_t plane = (static_cast<size_t>(b) * c.H + h) * c.N;
-  int32_t* n_moves = p.n_moves + static_cast<size_t>(b) * c.H + h;
-  if (n <= p.keep) {
-    if (threadIdx.x == 0) *n_moves = 0;
-    return;
-  }
-  const int keep_from = c.seq[kSeqTotal * c.B + b] - p.recent;
-  auto key_of = [&](int j) {
-    return evict_key(c.weight[plane + j], c.pos[plane + j], p.first, keep_from);
-  };
-  __shared__ int hist[256];
-  __shared__ unsigned s_prefix;
-  __shared__ int s_left;
-  unsigned prefix = 0;
-  int left = p.keep;  // rows still to be found among those that match the prefix
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = threadIdx.x; i < 256; i += 1024) hist[i] = 0;
-    __syncthreads();
-    const unsigned mask = shift == 24 ? 0u : ~0u << (shift + 8);
-    for (int j = threadIdx.x; j < n; j += 1024) {
-      const unsigned k = key_of(j);
-      if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255], 1);
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      int l = left, i = 255;
-      while (l > hist[i]) l -= hist[i--];
-      s_prefix = prefix | (static_cast<unsigned>(i) << shift);
-      s_left = l;
-    }
-    __syncthreads();
-    prefix = s_prefix;
-    left = s_left;
-    __syncthreads();
-  }
-  // prefix: the keep-th largest key; the first `left` rows that equal it stay
-  __shared__ int warp_sum[3][32];
-  int base_eq = 0, base_hole = 0, base_move = 0;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int32_t* holes = p.lists + plane;
-  int32_t* movers = holes + c.N / 2;
-  auto block_scan = [&](int which, bool flag, int& total) {
-    const unsigned bal = __ballot_sync(~0u, flag);
-    if (lane == 0) warp_sum[which][warp] = __popc(bal);
-    __syncthreads();
-    int before = 0;
-    total = 0;
-    for (int i = 0; i < 32; ++i) {
-      const int v = warp_sum[which][i];
-      if (i < warp) before += v;
-      total += v;
-    }
-    __syncthreads();
-    return before + __popc(bal & ((1u << lane) - 1));
-  };
-  for (int j0 = 0; j0 < n; j0 += 1024) {
-    const int j = j0 + threadIdx.x;
-    const unsigned k = j < n ? key_of(j) : 0u;
-    const bool eq = j < n && k == prefix;
-    int total;
-    const int rank = base_eq + block_scan(0, eq, total);
-    base_eq += total;
-    const bool kept = j < n && (k > prefix || (eq && rank < left));
-    const bool hole = j < p.keep && !kept, mover = j >= p.keep && kept;
-    const int at_h = base_hole + block_scan(1, hole, total);
-    base_hole += total;
-    const int at_m = base_move + block_scan(2, mover, total);
-    base_move += total;
-    if (hole) holes[at_h] = j;
-    if (mover) movers[at_m] = j;
-  }
-  if (threadIdx.x == 0) *n_moves = base_move;
-}
-
-// One row per 16 lanes: 16-byte pieces of codes, then scales, position and weight.
-// Block (0, 0, 0) sets seq, which no block reads here.
+// grid (cluster, H, B), 1024 threads.
 template <int D>
-__global__ void __launch_bounds__(256) kv4_evict_move_kernel(
-    const __grid_constant__ Kv4EvictParams p) {
+__global__ void __launch_bounds__(1024, 1)
+    kv4_evict_kernel(const __grid_constant__ Kv4EvictParams p) {
+  namespace cg = cooperative_groups;
+  cg::cluster_group cluster = cg::this_cluster();
+  extern __shared__ int smem_ints[];
+  int* copies = smem_ints;                   // [kEvictCopies][1024], the first pass
+  int* hist = copies + kEvictCopies * 1024;  // 1024 bins, then twice 2048
+  int* coarse = smem_ints + kEvictHist;      // [3][32]: sums of 32 (64) bins
+  int* s_pick = coarse + 96;                 // bin, rows left; holes, movers of this block
+  long long* s_warp = reinterpret_cast<long long*>(s_pick + 64);  // [2][32]
+  unsigned* s_key = reinterpret_cast<unsigned*>(s_warp + 64);
   const Kv4& c = p.c;
   const int h = blockIdx.y, b = blockIdx.z;
+  const int rank = static_cast<int>(cluster.block_rank());
+  const int blocks = static_cast<int>(cluster.num_blocks());
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const unsigned below_lane = (1u << lane) - 1;
+  const int n = rows_held(c, b);
   const size_t plane = (static_cast<size_t>(b) * c.H + h) * c.N;
-  const int n = p.n_moves[static_cast<size_t>(b) * c.H + h];
-  const int32_t* holes = p.lists + plane;
-  const int32_t* movers = holes + c.N / 2;
-  constexpr int kPieces = D / 32;  // 16-byte pieces of one code row
-  const int sub = threadIdx.x & 15;
-  for (int i = blockIdx.x * 16 + (threadIdx.x >> 4); i < n; i += gridDim.x * 16) {
-    const size_t to = plane + holes[i], from = plane + movers[i];
-    if (sub < kPieces) {
-      reinterpret_cast<uint4*>(c.k_codes + to * (D / 2))[sub] =
-          reinterpret_cast<const uint4*>(c.k_codes + from * (D / 2))[sub];
-    } else if (sub < 2 * kPieces) {
-      reinterpret_cast<uint4*>(c.v_codes + to * (D / 2))[sub - kPieces] =
-          reinterpret_cast<const uint4*>(c.v_codes + from * (D / 2))[sub - kPieces];
-    } else if (sub < 2 * kPieces + D / 64) {
-      const int s = sub - 2 * kPieces;
-      reinterpret_cast<uint32_t*>(c.k_scales + to * (D / 16))[s] =
-          reinterpret_cast<const uint32_t*>(c.k_scales + from * (D / 16))[s];
-    } else if (sub < 2 * kPieces + D / 32) {
-      const int s = sub - 2 * kPieces - D / 64;
-      reinterpret_cast<uint32_t*>(c.v_scales + to * (D / 16))[s] =
-          reinterpret_cast<const uint32_t*>(c.v_scales + from * (D / 16))[s];
-    } else if (sub == 14) {
-      c.pos[to] = c.pos[from];
-    } else if (sub == 15) {
-      c.weight[to] = c.weight[from];
+
+  // The warps' ordered scan of a pair of counts (low and high word): the sum over lower
+  // warps, and the block's total. `buffer`: 0 and 1 in turn, so one barrier does.
+  auto scan_warps = [&](int buffer, long long mine, long long& total) {
+    if (lane == 0) s_warp[buffer * 32 + warp] = mine;
+    __syncthreads();
+    long long x = s_warp[buffer * 32 + lane];
+    const long long own = x;
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+      const long long y = __shfl_up_sync(~0u, x, k);
+      if (lane >= k) x += y;
     }
-  }
-  if (blockIdx.x == 0 && h == 0 && b == 0) {
-    for (int i = threadIdx.x; i < c.B; i += 256) {
-      const int held = rows_held(c, i);
-      if (held > p.keep) {
-        c.seq[kSeqHeld * c.B + i] = p.keep;
-        c.seq[kSeqLast * c.B + i] = 0;
-        c.seq[kSeqTail * c.B + i] = 0;
+    total = __shfl_sync(~0u, x, 31);
+    return __shfl_sync(~0u, x - own, warp);
+  };
+
+  if (n > p.keep) {
+    const int keep_from = c.seq[kSeqTotal * c.B + b] - p.recent;
+    // rows of a warp, a multiple of 32 so that loads start on whole lines
+    const int per_warp = ((n + blocks * 32 - 1) / (blocks * 32) + 31) / 32 * 32;
+    const int j0 = min((rank * 32 + warp) * per_warp, n);
+    const int j1 = min(j0 + per_warp, n);
+    auto compute_key = [&](int j) {
+      return evict_key(__ldg(c.weight + plane + j), __ldg(c.pos + plane + j), p.first, keep_from);
+    };
+    const int slot0 = warp * per_warp - j0;  // key slot of row j: slot0 + j
+    auto key_of = [&](int j) {
+      return slot0 + j < p.smem_keys ? s_key[slot0 + j] : compute_key(j);
+    };
+    // four loads of each kind under way at a time
+    const int in_smem = min(j1, p.smem_keys - slot0);
+    for (int j = j0 + lane; j < in_smem; j += 128) {
+      float w[4];
+      int at[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (j + 32 * k < in_smem) {
+          w[k] = __ldg(c.weight + plane + j + 32 * k);
+          at[k] = __ldg(c.pos + plane + j + 32 * k);
+        }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (j + 32 * k < in_smem)
+          s_key[slot0 + j + 32 * k] = evict_key(w[k], at[k], p.first, keep_from);
+    }
+    for (int i = threadIdx.x; i < kEvictHist; i += 1024) smem_ints[i] = 0;
+    __syncthreads();
+
+    unsigned prefix = 0;
+    int left = p.keep;  // rows still to find among those that match the prefix
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 22 : pass == 1 ? 11 : 0;
+      const int above = pass == 1 ? 22 : 11;
+      int* mine = hist + (pass == 0 ? 0 : 1024 + (pass - 1) * 2048);
+      int* count = pass == 0 ? copies + (lane & (kEvictCopies - 1)) * 1024 : mine;
+      for (int j = j0 + lane; j < j1; j += 32) {
+        const unsigned k = key_of(j);
+        if (pass == 0 || k >> above == prefix) atomicAdd(&count[(k >> shift) & 2047u], 1);
+      }
+      __syncthreads();
+      const int per = pass == 0 ? 32 : 64;  // bins of a coarse sum, one sum a warp
+      int sum = 0;
+      if (pass == 0) {
+#pragma unroll
+        for (int k = 0; k < kEvictCopies; ++k) sum += copies[k * 1024 + threadIdx.x];
+        mine[threadIdx.x] = sum;
+      } else {
+        sum = mine[warp * 64 + lane] + mine[warp * 64 + 32 + lane];
+      }
+#pragma unroll
+      for (int k = 16; k; k >>= 1) sum += __shfl_xor_sync(~0u, sum, k);
+      if (lane == 0) coarse[pass * 32 + warp] = sum;
+      cluster.sync();
+      if (warp == 0) {
+        // Counts from the top, one of `width` neighbours a lane: the lane in which the
+        // left-th row from the top lies.
+        int need = left;
+        auto search = [&](const int* sums, int from, int width) {
+          const int i = from + width - 1 - lane;
+          int v = 0;
+          if (lane < width)
+            for (int r = 0; r < blocks; ++r) v += cluster.map_shared_rank(sums, r)[i];
+          int x = v;
+#pragma unroll
+          for (int k = 1; k < 32; k <<= 1) {
+            const int y = __shfl_up_sync(~0u, x, k);
+            if (lane >= k) x += y;
+          }
+          const unsigned enough = __ballot_sync(~0u, x >= need);
+          const int at = enough ? __ffs(enough) - 1 : -1;  // -1: not among these
+          const int before = __shfl_sync(~0u, x - v, at < 0 ? 31 : at);
+          const int all = __shfl_sync(~0u, x, 31);
+          need -= at < 0 ? all : before;
+          return at < 0 ? -1 : from + width - 1 - at;
+        };
+        const int block = search(coarse + pass * 32, 0, 32);
+        int bin = search(mine, (block + 1) * per - 32, 32);
+        if (bin < 0) bin = search(mine, block * per, 32);
+        if (lane == 0) {
+          s_pick[0] = bin;
+          s_pick[1] = need;
+        }
+      }
+      __syncthreads();
+      prefix = (prefix << 11) | static_cast<unsigned>(s_pick[0]);
+      left = s_pick[1];
+    }
+    // prefix: the keep-th largest key; the first `left` rows that equal it stay.
+    int equal_before = 0;  // such rows in lower blocks: their last histograms tell
+    for (int r = 0; r < rank; ++r)
+      equal_before += cluster.map_shared_rank(hist + 3072, r)[prefix & 2047u];
+    int more[2] = {0, 0}, equal[2] = {0, 0};  // below `keep` and from it on
+    for (int j = j0; j < j1; j += 32) {
+      const bool in = j + lane < j1;
+      const unsigned k = in ? key_of(j + lane) : 0u;
+      const unsigned gt = __ballot_sync(~0u, in && k > prefix);
+      const unsigned eq = __ballot_sync(~0u, in && k == prefix);
+      const int split = min(max(p.keep - j, 0), 32);  // lanes below `keep`
+      const unsigned low = split == 32 ? ~0u : (1u << split) - 1;
+      more[0] += __popc(gt & low);
+      more[1] += __popc(gt & ~low);
+      equal[0] += __popc(eq & low);
+      equal[1] += __popc(eq & ~low);
+    }
+    long long total;
+    equal_before += static_cast<int>(scan_warps(0, equal[0] + equal[1], total));
+    const int stay0 = min(max(left - equal_before, 0), equal[0]);
+    const int stay1 = min(max(left - equal_before - equal[0], 0), equal[1]);
+    const int my_holes = min(max(p.keep - j0, 0), j1 - j0) - more[0] - stay0;
+    const int my_movers = more[1] + stay1;
+    const long long below =
+        scan_warps(1, static_cast<long long>(my_movers) << 32 | my_holes, total);
+    int holes = static_cast<int>(below), movers = static_cast<int>(below >> 32);
+    if (threadIdx.x == 0) {
+      s_pick[2] = static_cast<int>(total);
+      s_pick[3] = static_cast<int>(total >> 32);
+    }
+    cluster.sync();
+    int moves = 0;
+    for (int r = 0; r < blocks; ++r) {
+      const int* other = cluster.map_shared_rank(s_pick, r);
+      if (r < rank) {
+        holes += other[2];
+        movers += other[3];
+      }
+      moves += other[3];
+    }
+    int32_t* hole_list = p.lists + plane;
+    int32_t* mover_list = hole_list + c.N / 2;
+    if (my_holes + my_movers > 0) {
+      int seen = equal_before;
+      for (int j = j0; j < j1; j += 32) {
+        const bool in = j + lane < j1, low = j + lane < p.keep;
+        const unsigned k = in ? key_of(j + lane) : 0u;
+        const unsigned eq = __ballot_sync(~0u, in && k == prefix);
+        const bool kept =
+            in && (k > prefix || (k == prefix && seen + __popc(eq & below_lane) < left));
+        seen += __popc(eq);
+        const unsigned hole = __ballot_sync(~0u, in && low && !kept);
+        const unsigned mover = __ballot_sync(~0u, !low && kept);
+        if (hole >> lane & 1u) hole_list[holes + __popc(hole & below_lane)] = j + lane;
+        if (mover >> lane & 1u) mover_list[movers + __popc(mover & below_lane)] = j + lane;
+        holes += __popc(hole);
+        movers += __popc(mover);
       }
     }
+    cluster.sync();  // lists written; no block reads another's shared memory from here
+
+    // 16 threads a row: 16-byte pieces of codes, 4-byte ones of scales, position and
+    // weight; four rows of each under way at a time.
+    constexpr int kPieces = D / 32, kScaleWords = D / 64;
+    const int sub = threadIdx.x & 15;
+    uint8_t* base = nullptr;  // this thread's array, its piece and bytes of a row
+    int row_bytes = 0, piece = 0;
+    if (sub < 2 * kPieces) {
+      base = sub < kPieces ? c.k_codes : c.v_codes;
+      row_bytes = D / 2;
+      piece = sub % kPieces * 16;
+    } else if (sub < 2 * kPieces + 2 * kScaleWords) {
+      const int s = sub - 2 * kPieces;
+      base = s < kScaleWords ? c.k_scales : c.v_scales;
+      row_bytes = D / 16;
+      piece = s % kScaleWords * 4;
+    } else if (sub >= 14) {
+      base = reinterpret_cast<uint8_t*>(sub == 14 ? static_cast<void*>(c.pos) : c.weight);
+      row_bytes = 4;
+    }
+    base += plane * row_bytes + piece;
+    for (int i = rank * 64 + (threadIdx.x >> 4); i < moves; i += blocks * 256) {
+      int from[4], to[4];
+      uint4 v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int at = i + k * blocks * 64;
+        from[k] = at < moves ? mover_list[at] : -1;
+        to[k] = at < moves ? hole_list[at] : -1;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (from[k] >= 0 && row_bytes != 0) {
+          const uint8_t* src = base + static_cast<size_t>(from[k]) * row_bytes;
+          if (sub < 2 * kPieces)
+            v[k] = *reinterpret_cast<const uint4*>(src);
+          else
+            v[k].x = *reinterpret_cast<const uint32_t*>(src);
+        }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (from[k] >= 0 && row_bytes != 0) {
+          uint8_t* dst = base + static_cast<size_t>(to[k]) * row_bytes;
+          if (sub < 2 * kPieces)
+            *reinterpret_cast<uint4*>(dst) = v[k];
+          else
+            *reinterpret_cast<uint32_t*>(dst) = v[k].x;
+        }
+    }
   }
+
+  // the last block to finish moves seq on: every block has read it by then
+  __shared__ bool s_last;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    s_last = atomicAdd(c.status + 2, 1u) == gridDim.x * gridDim.y * gridDim.z - 1;
+  }
+  __syncthreads();
+  if (!s_last) return;
+  for (int i = threadIdx.x; i < c.B; i += 1024)
+    if (rows_held(c, i) > p.keep) {
+      c.seq[kSeqHeld * c.B + i] = p.keep;
+      c.seq[kSeqLast * c.B + i] = 0;
+      c.seq[kSeqTail * c.B + i] = 0;
+    }
+  if (threadIdx.x == 0) c.status[2] = 0;  // ready for the next launch
 }
 
 }  // namespace sa

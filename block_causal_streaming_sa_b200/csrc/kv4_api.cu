@@ -325,8 +325,38 @@ bool launch_chunk(const sa::Kv4AttendParams& p, cudaStream_t s) {
 }
 
 size_t evict_bytes(const sa_kv4_cache* c) {
-  const size_t planes = static_cast<size_t>(c->batch) * c->kv_heads;
-  return align_up(planes * 4, 256) + planes * c->capacity * 4;
+  return align_up(static_cast<size_t>(c->batch) * c->kv_heads * c->capacity * sizeof(int32_t), 256);
+}
+
+// Blocks that share one head's rows: as many as leave each 4096 rows or more, while
+// all heads' blocks still run at once (two an SM).
+int evict_cluster(const Kv4& c) {
+  int n = 1;
+  while (n < 8 && n * 2 * 4096 <= c.N && 1LL * c.B * c.H * n * 2 <= 2LL * sm_count()) n *= 2;
+  return n;
+}
+
+template <int D>
+cudaError_t launch_evict(sa::Kv4EvictParams p, cudaStream_t s) {
+  constexpr int kMostKeys = 40960;  // 160 KB
+  const int cluster = evict_cluster(p.c);
+  const int per_block = ((p.c.N + cluster * 32 - 1) / (cluster * 32) + 31) / 32 * 32 * 32;
+  p.smem_keys = std::min(per_block, kMostKeys);
+  if (!allow_smem<sa::kv4_evict_kernel<D>>(sa::kEvictFixedSmem + kMostKeys * 4))
+    return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(cluster, p.c.H, p.c.B);
+  cfg.blockDim = dim3(1024);
+  cfg.dynamicSmemBytes = sa::kEvictFixedSmem + p.smem_keys * 4;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = cluster;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, sa::kv4_evict_kernel<D>, p);
 }
 
 }  // namespace
@@ -494,20 +524,15 @@ SA_API int sa_kv4_evict(const sa_kv4_cache* c, int keep, int first, int recent, 
   p.keep = keep;
   p.first = first;
   p.recent = recent;
-  p.n_moves = static_cast<int32_t*>(workspace);
-  p.lists = reinterpret_cast<int32_t*>(
-      static_cast<uint8_t*>(workspace) +
-      align_up(static_cast<size_t>(p.c.B) * p.c.H * sizeof(int32_t), 256));
+  p.lists = static_cast<int32_t*>(workspace);
   DeviceGuard guard(device);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  sa::kv4_evict_select_kernel<<<dim3(p.c.H, p.c.B), 1024, 0, s>>>(p);
-  const int most = std::min(keep, p.c.N - keep);  // rows that can move, a head
-  const dim3 grid(std::min((most + 15) / 16, 512), p.c.H, p.c.B);
-  if (c->head_dim == 128)
-    sa::kv4_evict_move_kernel<128><<<grid, 256, 0, s>>>(p);
-  else
-    sa::kv4_evict_move_kernel<64><<<grid, 256, 0, s>>>(p);
-  return launched("eviction");
+  const cudaError_t e = c->head_dim == 128 ? launch_evict<128>(p, s) : launch_evict<64>(p, s);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return refuse(SA_ERR_CUDA, std::string("eviction launch: ") + cudaGetErrorString(e));
+  }
+  return SA_OK;
 }
 
 SA_API int sa_kv4_get_status(const sa_kv4_cache* c, sa_stream stream) {
