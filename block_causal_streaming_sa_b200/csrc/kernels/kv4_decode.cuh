@@ -12,8 +12,8 @@
 //    along D is free as long as both operands agree, so a lane's K registers are the
 //    codes of one aligned 16-byte (D = 64: 8-byte) piece of a row, in order.
 //  * O^T = V^T P^T: 16 values x 8 query rows x 16 cache rows. A lane owns D / 8
-//    consecutive values of four rows; two rows' codes are interleaved by byte
-//    permutes after the conversion. P^T comes from S^T by transposing 8 x 8 blocks
+//    consecutive values of four rows; two rows' codes are merged into bytes before
+//    the conversion, which then yields pairs of rows. P^T comes from S^T by transposing 8 x 8 blocks
 //    (movmatrix); both keep query rows on the same lanes, so the softmax statistics
 //    never move.
 //  * The running maximum of a query row is raised only when a score exceeds it by
@@ -113,34 +113,64 @@ __device__ __forceinline__ int tile_row(int r) {
   return (r & 8) | static_cast<int>((order >> ((r & 7) * 4)) & 7u);
 }
 
-// Where the tiles of all (sequence, head, row block) units lie on the line. Every
-// block derives it from the lengths; lanes take a sequence each.
+// The tiles of all (sequence, head, row block) units lie on one line. Every warp derives
+// what it needs from the lengths, a sequence a lane.
 struct Line {
-  int share;        // tiles of a block
-  long long total;  // tiles in all
+  int share;  // tiles of a block: at least 4, so that every warp has one
+  int total;
 };
 
+// Tiles of one unit of sequence b.
 __device__ __forceinline__ int unit_tiles(const Kv4AttendParams& p, int b, int tile) {
-  if (tokens_of(p.counts, b, p.T) == 0) return 0;
+  if (b >= p.c.B || tokens_of(p.counts, b, p.T) == 0) return 0;
   return (rows_held(p.c, b) + tile - 1) / tile;
 }
 
-// Tiles of the sequences before `upto`, by a whole warp.
-__device__ __forceinline__ long long tiles_before(const Kv4AttendParams& p, int upto, int tile,
-                                                  int lane) {
-  long long sum = 0;
-  for (int b = lane; b < upto; b += 32) sum += unit_tiles(p, b, tile);
+__device__ __forceinline__ int scan_lanes(int x, int lane) {
 #pragma unroll
-  for (int k = 16; k; k >>= 1) sum += __shfl_xor_sync(~0u, sum, k);
-  return sum * p.c.H * p.row_blocks;
+  for (int k = 1; k < 32; k <<= 1) {
+    const int y = __shfl_up_sync(~0u, x, k);
+    if (lane >= k) x += y;
+  }
+  return x;
 }
 
-// At least 4 tiles a block, so that every warp has one.
 __device__ __forceinline__ Line line_of(const Kv4AttendParams& p, int blocks, int tile, int lane) {
+  int sum = 0;
+  for (int b = lane; b < p.c.B; b += 32) sum += unit_tiles(p, b, tile);
   Line l;
-  l.total = tiles_before(p, p.c.B, tile, lane);
-  l.share = static_cast<int>(max((l.total + blocks - 1) / blocks, 4LL));
+  l.total = __reduce_add_sync(~0u, sum) * p.c.H * p.row_blocks;
+  l.share = max((l.total + blocks - 1) / blocks, 4);
   return l;
+}
+
+// The sequence that holds tile `at` of the line (at < total), its first tile and the
+// tiles of one of its units.
+__device__ __forceinline__ void find_sequence(const Kv4AttendParams& p, int at, int tile, int lane,
+                                              int& b, int& begin, int& per_unit) {
+  const int units = p.c.H * p.row_blocks;
+  int base = 0;
+  for (int b0 = 0;; b0 += 32) {
+    const int n = unit_tiles(p, b0 + lane, tile);
+    const int end = base + scan_lanes(n * units, lane);
+    const unsigned past = __ballot_sync(~0u, at < end);
+    if (past != 0 || b0 + 32 >= p.c.B) {
+      const int hit = past != 0 ? __ffs(past) - 1 : 31;
+      b = b0 + hit;
+      begin = __shfl_sync(~0u, end - n * units, hit);
+      per_unit = __shfl_sync(~0u, n, hit);
+      return;
+    }
+    base = __shfl_sync(~0u, end, 31);
+  }
+}
+
+// Tiles of the line before sequence `upto`.
+__device__ __forceinline__ int tiles_before(const Kv4AttendParams& p, int upto, int tile,
+                                            int lane) {
+  int sum = 0;
+  for (int b = lane; b < upto; b += 32) sum += unit_tiles(p, b, tile);
+  return __reduce_add_sync(~0u, sum) * p.c.H * p.row_blocks;
 }
 
 template <int D, int NT, int kDtype, bool kScores>
@@ -167,35 +197,25 @@ __global__ void __launch_bounds__(128, DecodeShape<D, NT>::kBlocksPerSm)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   const Line line = line_of(p, gridDim.x, S::kTile, lane);
-  long long at = static_cast<long long>(blockIdx.x) * line.share;
-  const long long stop = min(at + line.share, line.total);
+  int at = min(static_cast<long long>(blockIdx.x) * line.share,
+               static_cast<long long>(line.total));
+  const int stop = min(at + line.share, line.total);
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b < c.B; b += 128) check_order(p, b, tokens_of(p.counts, b, p.T));
   if (at >= stop) return;
 
-  // the sequence that holds tile `at`
-  int b = 0;
-  long long b0 = 0;  // first tile of sequence b
-  while (true) {
-    const long long n = 1LL * unit_tiles(p, b, S::kTile) * c.H * p.row_blocks;
-    if (at < b0 + n) break;
-    b0 += n;
-    ++b;
-  }
+  int b, b0, per_unit;  // the sequence of tile `at`, its first tile, tiles of a unit
+  find_sequence(p, at, S::kTile, lane, b, b0, per_unit);
   unsigned loads = 0, uses = 0;  // stages filled and emptied so far by this warp
   bool ok = true;
 
   while (at < stop) {
-    // one unit: rows [t0, t1) tiles of sequence b, KV head h, query rows row0 ..
-    const int per_unit = unit_tiles(p, b, S::kTile);
-    if (per_unit == 0 || at >= b0 + 1LL * per_unit * c.H * p.row_blocks) {
-      b0 += 1LL * per_unit * c.H * p.row_blocks;
-      ++b;
-      continue;
-    }
-    const int unit_in_b = static_cast<int>((at - b0) / per_unit);
-    const int t0 = static_cast<int>((at - b0) % per_unit);
-    const int t1 = static_cast<int>(min(static_cast<long long>(per_unit), t0 + (stop - at)));
+    // one unit: tiles [t0, t1) of sequence b, KV head h, query rows row0 ..
+    if (at >= b0 + per_unit * c.H * p.row_blocks)
+      find_sequence(p, at, S::kTile, lane, b, b0, per_unit);
+    const int unit_in_b = (at - b0) / per_unit;
+    const int t0 = at - b0 - unit_in_b * per_unit;
+    const int t1 = min(per_unit, t0 + (stop - at));
     const int h = unit_in_b / p.row_blocks, rb = unit_in_b % p.row_blocks;
     const int unit = b * c.H * p.row_blocks + unit_in_b;
     const int held = rows_held(c, b), n_tok = tokens_of(p.counts, b, p.T);
@@ -439,39 +459,38 @@ __global__ void __launch_bounds__(128, DecodeShape<D, NT>::kBlocksPerSm)
       // D / 8 g .. (matrix rows g and g + 8 of tile k are values 2 k and 2 k + 1)
 #pragma unroll
       for (int sub = 0; sub < 2; ++sub) {
-        uint32_t vw[4][VW], sc[4];
+        uint32_t vw[4][VW], byte[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int row = sub * 16 + tile_row<D>(2 * tig + (e & 1) + 8 * (e >> 1));
-          uint32_t byte;
           if constexpr (D == 128) {
             const uint2 w = lds64(vc + row * 64 + g * 8);
             vw[e][0] = w.x;
             vw[e][VW - 1] = w.y;
-            byte = lds8(vsc + row * 8 + g);
+            byte[e] = lds8(vsc + row * 8 + g);
           } else {
             vw[e][0] = lds32(vc + row * 32 + g * 4);
-            byte = lds8(vsc + row * 4 + (g >> 1));
+            byte[e] = lds8(vsc + row * 4 + (g >> 1));
           }
           // rows not held may hold any bytes: a scale that is NaN must not meet P = 0
-          if (edge && j0 + row >= held) byte = 0;
-          sc[e] = scale_f16x2(byte);
+          if (edge && j0 + row >= held) byte[e] = 0;
         }
+        const uint32_t sc[2] = {scales_f16x2(byte[0], byte[1]), scales_f16x2(byte[2], byte[3])};
 #pragma unroll
         for (int w = 0; w < VW; ++w) {
-          uint32_t v[4][4];
+          // Two rows' codes of one value into a byte, so that the conversion leaves
+          // them as a pair: [rows 0 and 1, rows 2 and 3][even, odd values].
+          uint32_t v[2][2][4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            codes_to_f16(vw[e][w], v[e]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[e][i] = mul_f16x2(v[e][i], sc[e]);
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t x = vw[2 * e][w], y = vw[2 * e + 1][w];
+            codes_to_f16((x & 0x0F0F0F0Fu) | ((y * 16u) & 0xF0F0F0F0u), v[e][0]);
+            codes_to_f16(((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u), v[e][1]);
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint32_t a0 = __byte_perm(v[0][i], v[1][i], 0x5410);
-            const uint32_t a1 = __byte_perm(v[0][i], v[1][i], 0x7632);
-            const uint32_t a2 = __byte_perm(v[2][i], v[3][i], 0x5410);
-            const uint32_t a3 = __byte_perm(v[2][i], v[3][i], 0x7632);
+            const uint32_t a0 = mul_f16x2(v[0][0][i], sc[0]), a1 = mul_f16x2(v[0][1][i], sc[0]);
+            const uint32_t a2 = mul_f16x2(v[1][0][i], sc[1]), a3 = mul_f16x2(v[1][1][i], sc[1]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
               mma_16816(o[4 * w + i][nt], a0, a1, a2, a3, pb[sub][nt][0], pb[sub][nt][1]);
@@ -550,99 +569,123 @@ __global__ void __launch_bounds__(128, DecodeShape<D, NT>::kBlocksPerSm)
   }
 }
 
-// Merge of the partial results of kv4_decode_kernel, a warp per query row, and the
-// rows' weights. Blocks below join_blocks merge; the others add weights, `kKeys`
-// cache rows of one (sequence, KV head) each: they derive the log-sum-exp of its
-// query rows from the same partial results, so no order among blocks is needed.
+// Merge of the partial results of kv4_decode_kernel, W warps per query row, and the rows'
+// weights. Blocks below join_blocks merge; the others add weights, kJoinKeys cache
+// rows of one (sequence, KV head) each: they derive the log-sum-exp of its query rows
+// from the same partial results, so no order among blocks is needed.
 constexpr int kJoinKeys = 512;
 
-template <int D, int kRows, int kDtype>
+template <int D, int kRows, int W, int kDtype>
 __global__ void __launch_bounds__(128)
     kv4_join_kernel(const __grid_constant__ Kv4AttendParams p, int blocks, int join_blocks) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const Kv4& c = p.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool joins = static_cast<int>(blockIdx.x) < join_blocks;
-  // join: block = (unit, four rows of it); weights: block = (head plane, chunk of rows)
-  const int row_groups = kRows / 4;
+  // join: block = (unit, 4 / W rows of it); weights: block = (head plane, chunk of rows)
+  constexpr int kGroups = kRows * W / 4;
   const int chunks = (c.N + kJoinKeys - 1) / kJoinKeys;
-  const int id = joins ? blockIdx.x / row_groups : (blockIdx.x - join_blocks) / chunks;
+  const int id = joins ? blockIdx.x / kGroups : (blockIdx.x - join_blocks) / chunks;
   const int units_b = c.H * p.row_blocks;
   const int b = joins ? id / units_b : id / c.H;
+  // lengths were there before the decode kernel began: the schedule needs no wait
   const int held = rows_held(c, b), n_tok = tokens_of(p.counts, b, p.T);
   const int n_rows = n_tok * p.group;
-  if (n_rows == 0) return;
   const Line line = line_of(p, blocks, 32, lane);
-  const long long b0 = tiles_before(p, b, 32, lane);
+  const int b0 = tiles_before(p, b, 32, lane);
   const int per_unit = unit_tiles(p, b, 32);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (n_rows == 0) return;
 
-  // Partial results of one query row: slots first .. last (none: last < first).
-  auto slots_of = [&](int unit_in_b, size_t& first, size_t& last) {
-    const long long u0 = b0 + 1LL * unit_in_b * per_unit;
-    const size_t unit = static_cast<size_t>(b) * units_b + unit_in_b;
-    if (per_unit == 0) {
-      first = 1;
-      last = 0;
-      return;
-    }
-    first = u0 / line.share + unit;
-    last = (u0 + per_unit - 1) / line.share + unit;
-  };
-  auto statistics = [&](size_t first, size_t last, int r, float& mx, float& sum) {
-    mx = -INFINITY;
-    for (size_t s = first + lane; s <= last; s += 32) mx = fmaxf(mx, p.part_ml[s * kRows + r].x);
-#pragma unroll
-    for (int k = 16; k; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, k));
-    const float ref = mx == -INFINITY ? 0.f : mx;
-    sum = 0.f;
-    for (size_t s = first + lane; s <= last; s += 32) {
-      const float2 ml = p.part_ml[s * kRows + r];
-      sum += ml.y * ptx::ex2(ml.x - ref);
-    }
-#pragma unroll
-    for (int k = 16; k; k >>= 1) sum += __shfl_xor_sync(~0u, sum, k);
+  // Partial results of one query row: `n` slots from `first` on.
+  auto slots_of = [&](int unit_in_b, size_t& first, int& n) {
+    const int u0 = b0 + unit_in_b * per_unit;
+    first = static_cast<size_t>(u0 / line.share) + static_cast<size_t>(b) * units_b + unit_in_b;
+    n = per_unit == 0 ? 0 : (u0 + per_unit - 1) / line.share - u0 / line.share + 1;
   };
 
   if (joins) {
     const int unit_in_b = id % units_b;
     const int h = unit_in_b / p.row_blocks, rb = unit_in_b % p.row_blocks;
-    const int r = (blockIdx.x % row_groups) * 4 + warp;
+    const int part = warp % W;  // slots part, part + W, ..
+    const int r = (blockIdx.x % kGroups) * (4 / W) + warp / W;
     const int row = rb * kRows + r;
-    if (row >= n_rows) return;
-    size_t first, last;
-    slots_of(unit_in_b, first, last);
-    float mx, sum;
-    statistics(first, last, r, mx, sum);
-    const float ref = mx == -INFINITY ? 0.f : mx;
+    if (W == 1 && row >= n_rows) return;
+    size_t first;
+    int n;
+    slots_of(unit_in_b, first, n);
+    if (W > 1 && row >= n_rows) return;  // the whole block: a row
     constexpr int V = D / 32;
-    float acc[V];
+    float acc[V], mx = -INFINITY, sum = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.f;
-    for (size_t s = first; s <= last; s += 4) {
-      float x[4][V], a[4];
+    // 32 slots' statistics at a time, a slot a lane; eight rows of loads under way
+    const int mine = (n - part + W - 1) / W;
+    for (int s0 = 0; s0 < mine; s0 += 32) {
+      const int cnt = min(mine - s0, 32);
+      const size_t base = first + part + static_cast<size_t>(s0) * W;
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (lane < cnt) ml = p.part_ml[(base + static_cast<size_t>(lane) * W) * kRows + r];
+      float m_new = ml.x;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {  // four rows of loads under way at a time
-        const bool have = s + k <= last;
-        const size_t at = (have ? s + k : s) * kRows + r;
-        a[k] = have ? ptx::ex2(p.part_ml[at].x - ref) : 0.f;
-        const float* src = p.part_o + at * D + lane * V;
-        if constexpr (V == 4) {
-          const float4 v = *reinterpret_cast<const float4*>(src);
-          x[k][0] = v.x;
-          x[k][1] = v.y;
-          x[k][V - 2] = v.z;
-          x[k][V - 1] = v.w;
-        } else {
-          const float2 v = *reinterpret_cast<const float2*>(src);
-          x[k][0] = v.x;
-          x[k][1] = v.y;
+      for (int k = 16; k; k >>= 1) m_new = fmaxf(m_new, __shfl_xor_sync(~0u, m_new, k));
+      m_new = fmaxf(m_new, mx);
+      const float ref = m_new == -INFINITY ? 0.f : m_new;
+      const float old = ptx::ex2(mx - ref), a = ptx::ex2(ml.x - ref);
+      mx = m_new;
+      float add = ml.y * a;
+#pragma unroll
+      for (int k = 16; k; k >>= 1) add += __shfl_xor_sync(~0u, add, k);
+      sum = sum * old + add;
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] *= old;
+      for (int k0 = 0; k0 < cnt; k0 += 8) {
+        float x[8][V];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const size_t at = (base + static_cast<size_t>(min(k0 + k, cnt - 1)) * W) * kRows + r;
+          const float* src = p.part_o + at * D + lane * V;
+          if constexpr (V == 4) {
+            const float4 v = *reinterpret_cast<const float4*>(src);
+            x[k][0] = v.x;
+            x[k][1] = v.y;
+            x[k][V - 2] = v.z;
+            x[k][V - 1] = v.w;
+          } else {
+            const float2 v = *reinterpret_cast<const float2*>(src);
+            x[k][0] = v.x;
+            x[k][1] = v.y;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float ak = __shfl_sync(~0u, a, k0 + k & 31);
+          if (k0 + k < cnt)
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] = fmaf(x[k][i], ak, acc[i]);
         }
       }
+    }
+    if constexpr (W > 1) {  // the warps' parts, in order
+      __shared__ float s_acc[W][D];
+      __shared__ float2 s_ml[W];
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (s + k <= last)
+      for (int i = 0; i < V; ++i) s_acc[warp][lane * V + i] = acc[i];
+      if (lane == 0) s_ml[warp] = make_float2(mx, sum);
+      __syncthreads();
+      if (warp != 0) return;
 #pragma unroll
-          for (int i = 0; i < V; ++i) acc[i] = fmaf(x[k][i], a[k], acc[i]);
+      for (int w = 1; w < W; ++w) mx = fmaxf(mx, s_ml[w].x);
+      const float ref = mx == -INFINITY ? 0.f : mx;
+      sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] = 0.f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const float a = ptx::ex2(s_ml[w].x - ref);
+        sum += s_ml[w].y * a;
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = fmaf(s_acc[w][lane * V + i], a, acc[i]);
+      }
     }
     // a sum that is NaN (a query that is not finite) must stay NaN
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -666,11 +709,22 @@ __global__ void __launch_bounds__(128)
   if (j0 >= held) return;
   extern __shared__ float s_lse[];  // [score_rows]
   for (int row = warp; row < p.score_rows; row += 4) {
-    float mx = 0.f, sum = 0.f;
+    float mx = -INFINITY, sum = 0.f;
     if (row < n_rows) {
-      size_t first, last;
-      slots_of(h * p.row_blocks + row / kRows, first, last);
-      statistics(first, last, row % kRows, mx, sum);
+      size_t first;
+      int n;
+      slots_of(h * p.row_blocks + row / kRows, first, n);
+      const float2* ml = p.part_ml + first * kRows + row % kRows;
+      for (int s = lane; s < n; s += 32) mx = fmaxf(mx, ml[static_cast<size_t>(s) * kRows].x);
+#pragma unroll
+      for (int k = 16; k; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, k));
+      const float ref = mx == -INFINITY ? 0.f : mx;
+      for (int s = lane; s < n; s += 32) {
+        const float2 x = ml[static_cast<size_t>(s) * kRows];
+        sum += x.y * ptx::ex2(x.x - ref);
+      }
+#pragma unroll
+      for (int k = 16; k; k >>= 1) sum += __shfl_xor_sync(~0u, sum, k);
     }
     // rows that are not there, or see nothing, add 0
     if (lane == 0) s_lse[row] = row < n_rows && sum != 0.f ? mx + log2f(sum) : INFINITY;

@@ -99,9 +99,11 @@ __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t (&h)[4]) {
       : "r"(w));
 }
 
-// A scale byte as an fp16 pair.
-__device__ __forceinline__ uint32_t scale_f16x2(uint32_t byte) {
-  return (byte << 7) * 0x00010001u;
+// A scale byte as an fp16 pair, and two as the halves of one (multiplications: the
+// pipe that shifts and selects is the one the conversions load).
+__device__ __forceinline__ uint32_t scale_f16x2(uint32_t byte) { return byte * 0x00800080u; }
+__device__ __forceinline__ uint32_t scales_f16x2(uint32_t lo, uint32_t hi) {
+  return hi * 0x00800000u + lo * 0x80u;
 }
 
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {

@@ -158,7 +158,8 @@ int check_heads(const sa_kv4_cache* c, int heads, int T) {
     return refuse(SA_ERR_INVALID_ARG, "heads must be a multiple of kv_heads");
   const long long rows = 1LL * (heads / c->kv_heads) * T;
   if (heads > kMaxGridYZ || rows > (1LL << 30) ||
-      (rows + 255) / 256 * (c->capacity / 128) > INT32_MAX)
+      (rows + 255) / 256 * (c->capacity / 128) > INT32_MAX ||
+      1LL * c->batch * c->kv_heads * (c->capacity / 32) > INT32_MAX / 4)
     return refuse(SA_ERR_UNSUPPORTED, "too many query rows");
   return SA_OK;
 }
@@ -285,11 +286,19 @@ bool launch_decode(const sa::Kv4AttendParams& p, cudaStream_t s) {
   if (!allow_smem<sa::kv4_decode_kernel<D, NT, kDtype, kScores>>(S::kSmem)) return false;
   const int blocks = std::min(sm_count(), kMostSms) * S::kBlocksPerSm;
   sa::kv4_decode_kernel<D, NT, kDtype, kScores><<<blocks, 128, S::kSmem, s>>>(p);
-  const int join = p.c.B * p.c.H * p.row_blocks * (S::kRows / 4);
+  const int units = p.c.B * p.c.H * p.row_blocks;
   const int chunks = (p.c.N + sa::kJoinKeys - 1) / sa::kJoinKeys;
-  const int grid = join + (kScores ? p.c.B * p.c.H * chunks : 0);
-  launch_after(sa::kv4_join_kernel<D, S::kRows, kDtype>, dim3(grid), dim3(128),
-               p.score_rows * sizeof(float), s, p, blocks, join);
+  // Long rows leave many partial results: a block merges one query row's. With 8 or
+  // fewer a warp a row is enough.
+  auto join = [&](auto kernel, int warps) {
+    const int merge = units * (S::kRows * warps / 4);
+    launch_after(kernel, dim3(merge + (kScores ? p.c.B * p.c.H * chunks : 0)), dim3(128),
+                 p.score_rows * sizeof(float), s, p, blocks, merge);
+  };
+  if (blocks > 8 * units)
+    join(sa::kv4_join_kernel<D, S::kRows, 4, kDtype>, 4);
+  else
+    join(sa::kv4_join_kernel<D, S::kRows, 1, kDtype>, 1);
   return true;
 }
 
