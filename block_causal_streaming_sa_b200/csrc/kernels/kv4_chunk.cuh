@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int k = 0; k < 4; ++k) x[k] = pack2<SA_DTYPE_FP16>(v[k].x * f, v[k].y * f);
     *reinterpret_cast<uint4*>(dst + tile_offset(r, piece)) = make_uint4(x[0], x[1], x[2], x[3]);
-    if (piece == 0) p.row_scale[tile_id * 128 + r] = row < n_rows ? p.scale_log2 / f : 0.f;
+    if (piece == 0) p.row_scale[tile_id * 128 + r] = row < n_rows ? score_factor(p.scale_log2, f) : 0.f;
     if (row >= n_rows) {
       if (piece == 0) p.row_nlse[tile_id * 128 + r] = -INFINITY;  // such rows draw no weight
     } else if (empty) {

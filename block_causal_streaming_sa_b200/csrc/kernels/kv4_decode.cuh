@@ -32,6 +32,10 @@
 
 namespace sa {
 
+// The running maximum before any score: finite, so that a masked score (-inf) minus it
+// is -inf, and below every score.
+constexpr float kNoScore = -3.402823466e38f;
+
 template <int D, int NT>
 struct DecodeShape {
   static constexpr int kWarps = 4;
@@ -206,8 +210,13 @@ __global__ void __launch_bounds__(128, DecodeShape<D, NT>::kBlocksPerSm)
 
   int b, b0, per_unit;  // the sequence of tile `at`, its first tile, tiles of a unit
   find_sequence(p, at, S::kTile, lane, b, b0, per_unit);
-  unsigned loads = 0, uses = 0;  // stages filled and emptied so far by this warp
+  int st = 0, pending = 0;  // stage in turn; copies under way or not used yet
+  uint32_t phase = 0;
   bool ok = true;
+  const int copy_at = lane == 0   ? 0
+                      : lane == 1 ? S::kCodes
+                      : lane == 2 ? 2 * S::kCodes
+                                  : 2 * S::kCodes + S::kScales;
 
   while (at < stop) {
     // one unit: tiles [t0, t1) of sequence b, KV head h, query rows row0 ..
@@ -222,19 +231,38 @@ __global__ void __launch_bounds__(128, DecodeShape<D, NT>::kBlocksPerSm)
     const int n_rows = n_tok * p.group, row0 = rb * S::kRows;
     const size_t plane = (static_cast<size_t>(b) * c.H + h) * c.N;
 
-    auto fill = [&](int tile) {  // lane 0
-      const unsigned s = loads % S::kStages;
-      const uint32_t dst = ring + s * S::kStageBytes, bar = bars + 8 * s;
-      const size_t row = plane + static_cast<size_t>(tile) * S::kTile;
-      ptx::mbar_arrive_expect_tx(bar, S::kStageBytes);
-      bulk_load(dst, c.k_codes + row * (D / 2), S::kCodes, bar);
-      bulk_load(dst + S::kCodes, c.v_codes + row * (D / 2), S::kCodes, bar);
-      bulk_load(dst + 2 * S::kCodes, c.k_scales + row * (D / 16), S::kScales, bar);
-      bulk_load(dst + 2 * S::kCodes + S::kScales, c.v_scales + row * (D / 16), S::kScales, bar);
+    // Lanes 0 .. 3 each issue one of a tile's four copies, from `src` on.
+    const int copy_bytes = lane < 2 ? S::kCodes : S::kScales;
+    const uint8_t* src = (lane == 0   ? c.k_codes
+                          : lane == 1 ? c.v_codes
+                          : lane == 2 ? c.k_scales
+                                      : c.v_scales) +
+                         plane * (lane < 2 ? D / 2 : D / 16);
+    auto fill = [&](int tile, int stage) {
+      const uint32_t bar = bars + 8 * stage;
+      if (lane == 0) ptx::mbar_arrive_expect_tx(bar, S::kStageBytes);
+      __syncwarp();
+      if (lane < 4)
+        bulk_load(ring + stage * S::kStageBytes + copy_at, src + static_cast<size_t>(tile) * copy_bytes,
+                  copy_bytes, bar);
     };
-    int next = t0 + warp;  // next tile to load
-    for (int s = 0; ok && s < S::kStages && next < t1; ++s, next += S::kWarps, ++loads)
-      if (lane == 0) fill(next);
+    // The query row of this lane is asked for before the ring is filled: behind 200 KB of
+    // copies an SM it would come microseconds later. Warps share the rows of NT > 1.
+    const int my_nt = NT == 1 ? 0 : warp, q_row = row0 + my_nt * 8 + g;
+    const bool has_row = my_nt < NT && q_row < n_rows;
+    uint4 qw[D / 32];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) qw[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (has_row) {
+      const uint16_t* q = static_cast<const uint16_t*>(p.q.data) + b * p.q.sb +
+                          (q_row / p.group) * p.q.st +
+                          (h * p.group + q_row % p.group) * p.q.sh + tig * (D / 4);
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) qw[i] = __ldg(reinterpret_cast<const uint4*>(q) + i);
+    }
+    int next = t0 + warp;  // next tile to load; the ring is empty here
+    for (int s = 0; s < S::kStages && ok && next < t1; ++s, next += S::kWarps, ++pending)
+      fill(next, st + s < S::kStages ? st + s : st + s - S::kStages);
 
     // Query fragments: lane (g, tig) of step k holds values 4 k .. 4 k + 3 of its
     // D / 4 consecutive ones of query row g. Scaled to fp16 by a power of two a row.
@@ -242,32 +270,18 @@ __global__ void __launch_bounds__(128, DecodeShape<D, NT>::kBlocksPerSm)
     float sl[NT][2];  // scale * log2 e / row factor of this lane's query columns
     float* s_sl = reinterpret_cast<float*>(smem + S::kOffSl);
     if constexpr (NT > 1) __syncthreads();  // the previous unit is done with them
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      if (NT > 1 && nt % S::kWarps != warp) continue;
-      const int r = row0 + nt * 8 + g;
+    if (my_nt < NT) {
       float2 v[D / 8];
       float amax = 0.f;
-      if (r < n_rows) {
-        const uint16_t* src = static_cast<const uint16_t*>(p.q.data) + b * p.q.sb +
-                              (r / p.group) * p.q.st + (h * p.group + r % p.group) * p.q.sh +
-                              tig * (D / 4);
-        uint4 w[D / 32];
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(src) + i);
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          v[4 * i] = unpack2<kDtype>(w[i].x);
-          v[4 * i + 1] = unpack2<kDtype>(w[i].y);
-          v[4 * i + 2] = unpack2<kDtype>(w[i].z);
-          v[4 * i + 3] = unpack2<kDtype>(w[i].w);
-        }
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) amax = fmaxf(amax, fmaxf(fabsf(v[i].x), fabsf(v[i].y)));
-      } else {
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) v[i] = make_float2(0.f, 0.f);
+      for (int i = 0; i < D / 32; ++i) {
+        v[4 * i] = unpack2<kDtype>(qw[i].x);
+        v[4 * i + 1] = unpack2<kDtype>(qw[i].y);
+        v[4 * i + 2] = unpack2<kDtype>(qw[i].z);
+        v[4 * i + 3] = unpack2<kDtype>(qw[i].w);
       }
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) amax = fmaxf(amax, fmaxf(fabsf(v[i].x), fabsf(v[i].y)));
       amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 2));
       const float f = row_factor(amax);
@@ -279,16 +293,16 @@ __global__ void __launch_bounds__(128, DecodeShape<D, NT>::kBlocksPerSm)
           qf[k][0] = x;
           qf[k][1] = y;
         } else {
-          *reinterpret_cast<uint2*>(smem + S::kOffQ + ((k * NT + nt) * 32 + lane) * 8) =
+          *reinterpret_cast<uint2*>(smem + S::kOffQ + ((k * NT + my_nt) * 32 + lane) * 8) =
               make_uint2(x, y);
         }
       }
-      const float scale = p.scale_log2 / f;
+      const float scale = score_factor(p.scale_log2, f);
       if constexpr (NT == 1) {  // lane 4 n (or any of its four) holds row n's
         sl[0][0] = __shfl_sync(~0u, scale, 8 * tig);
         sl[0][1] = __shfl_sync(~0u, scale, 8 * tig + 4);
       } else {
-        if (tig == 0) s_sl[nt * 8 + g] = scale;
+        if (tig == 0) s_sl[my_nt * 8 + g] = scale;
       }
     }
     if constexpr (NT > 1) {
@@ -307,17 +321,16 @@ __global__ void __launch_bounds__(128, DecodeShape<D, NT>::kBlocksPerSm)
       for (int k = 0; k < KS; ++k)
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[k][nt][i] = 0.f;
-      m[nt][0] = m[nt][1] = -INFINITY;
+      m[nt][0] = m[nt][1] = kNoScore;
       l[nt][0] = l[nt][1] = 0.f;
     }
     // rows before this see no mask
     const int open = p.causal ? max(held - n_tok + 1, 0) : held;
 
     for (int t = t0 + warp; ok && t < t1; t += S::kWarps) {
-      const unsigned st = uses % S::kStages;
-      ok = ptx::mbar_wait(bars + 8 * st, (uses / S::kStages) & 1, abort_flag, c.status);
+      ok = __all_sync(~0u, ptx::mbar_wait(bars + 8 * st, phase, abort_flag, c.status));
       if (!ok) break;
-      ++uses;
+      --pending;
       const uint32_t kc = ring + st * S::kStageBytes, vc = kc + S::kCodes;
       const uint32_t ksc = vc + S::kCodes, vsc = ksc + S::kScales;
       const int j0 = t * S::kTile;
@@ -386,14 +399,9 @@ __global__ void __launch_bounds__(128, DecodeShape<D, NT>::kBlocksPerSm)
       }
 
       // ---- softmax: s[sub][nt] = rows g, g, g + 8, g + 8; queries 2 tig, 2 tig + 1, ..
-      bool raise = false;
+      if (edge) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int sub = 0; sub < 2; ++sub)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[sub][nt][i] *= sl[nt][i & 1];
-        if (edge) {
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int r = row0 + nt * 8 + 2 * tig + (i & 1);
@@ -403,13 +411,37 @@ __global__ void __launch_bounds__(128, DecodeShape<D, NT>::kBlocksPerSm)
               if (j0 + sub * 16 + tile_row<D>(g + (i & 2) * 4) >= end)
                 s[sub][nt][i] = -INFINITY;
           }
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          raise |= fmaxf(fmaxf(s[0][nt][i], s[0][nt][i + 2]), fmaxf(s[1][nt][i], s[1][nt][i + 2])) >
-                   m[nt][i] + 8.f;
       }
-      if (__any_sync(~0u, raise)) {
+      if constexpr (kScores) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int r = row0 + nt * 8 + 2 * tig;
+          if (r < p.score_rows)
+#pragma unroll
+            for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+              for (int hi = 0; hi < 2; ++hi) {
+                const size_t row = plane + j0 + sub * 16 + tile_row<D>(g + 8 * hi);
+                *reinterpret_cast<float2*>(p.scores + row * p.score_rows + r) =
+                    make_float2(s[sub][nt][2 * hi] * sl[nt][0], s[sub][nt][2 * hi + 1] * sl[nt][1]);
+              }
+        }
+      }
+      float x[2][NT][4];
+      auto subtract = [&]() {
+        float top = -INFINITY;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              x[sub][nt][i] = fmaf(s[sub][nt][i], sl[nt][i & 1], -m[nt][i & 1]);
+              top = fmaxf(top, x[sub][nt][i]);
+            }
+        return top;
+      };
+      if (__any_sync(~0u, subtract() > 8.f)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -418,7 +450,7 @@ __global__ void __launch_bounds__(128, DecodeShape<D, NT>::kBlocksPerSm)
                              fmaxf(s[1][nt][i], s[1][nt][i + 2]));
 #pragma unroll
             for (int k = 4; k < 32; k <<= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, k));
-            mx = fmaxf(mx, m[nt][i]);
+            mx = fmaxf(mx * sl[nt][i], m[nt][i]);
             const float a = mx > m[nt][i] ? ptx::ex2(m[nt][i] - mx) : 1.f;
             m[nt][i] = mx;
             l[nt][i] *= a;
@@ -428,32 +460,20 @@ __global__ void __launch_bounds__(128, DecodeShape<D, NT>::kBlocksPerSm)
               o[k][nt][i + 2] *= a;
             }
           }
+        subtract();
       }
       uint32_t pb[2][NT][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const float n0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
-        const float n1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int sub = 0; sub < 2; ++sub) {
-          if constexpr (kScores) {
-            const int r = row0 + nt * 8 + 2 * tig;
-            if (r < p.score_rows)
-#pragma unroll
-              for (int hi = 0; hi < 2; ++hi) {
-                const size_t row = plane + j0 + sub * 16 + tile_row<D>(g + 8 * hi);
-                *reinterpret_cast<float2*>(p.scores + row * p.score_rows + r) =
-                    make_float2(s[sub][nt][2 * hi], s[sub][nt][2 * hi + 1]);
-              }
-          }
-          const float p0 = ptx::ex2(s[sub][nt][0] - n0), p1 = ptx::ex2(s[sub][nt][1] - n1);
-          const float p2 = ptx::ex2(s[sub][nt][2] - n0), p3 = ptx::ex2(s[sub][nt][3] - n1);
+          const float p0 = ptx::ex2(x[sub][nt][0]), p1 = ptx::ex2(x[sub][nt][1]);
+          const float p2 = ptx::ex2(x[sub][nt][2]), p3 = ptx::ex2(x[sub][nt][3]);
           l[nt][0] += p0 + p2;
           l[nt][1] += p1 + p3;
           pb[sub][nt][0] = transpose_8x8(pack2<SA_DTYPE_FP16>(p0, p1));
           pb[sub][nt][1] = transpose_8x8(pack2<SA_DTYPE_FP16>(p2, p3));
         }
-      }
 
       // ---- O^T: a lane's rows are 2 tig, 2 tig + 1, and those + 8; its values
       // D / 8 g .. (matrix rows g and g + 8 of tile k are values 2 k and 2 k + 1)
@@ -498,10 +518,14 @@ __global__ void __launch_bounds__(128, DecodeShape<D, NT>::kBlocksPerSm)
         }
       }
       __syncwarp();  // every lane has read the stage
-      if (next < t1) {
-        if (lane == 0) fill(next);
+      if (next < t1) {  // the ring was full: this stage is the next to fill
+        fill(next, st);
         next += S::kWarps;
-        ++loads;
+        ++pending;
+      }
+      if (++st == S::kStages) {
+        st = 0;
+        phase ^= 1u;
       }
     }
     // (after an abort the blocks' barriers below are still met; the result is void)
@@ -564,8 +588,13 @@ __global__ void __launch_bounds__(128, DecodeShape<D, NT>::kBlocksPerSm)
   // after an abort: copies still under way land before the block's memory goes
   if (!ok) {
     volatile int none = 0;
-    for (; uses < loads; ++uses)
-      ptx::mbar_wait(bars + 8 * (uses % S::kStages), (uses / S::kStages) & 1, &none, c.status);
+    for (; pending > 0; --pending) {
+      ptx::mbar_wait(bars + 8 * st, phase, &none, c.status);
+      if (++st == S::kStages) {
+        st = 0;
+        phase ^= 1u;
+      }
+    }
   }
 }
 

@@ -6,6 +6,12 @@
 
 namespace sa {
 
+// What a staged row's scores are multiplied with. Kept above zero: a masked score is
+// -inf, and 0 * -inf is not.
+__device__ __forceinline__ float score_factor(const float scale_log2, float row_factor) {
+  return fmaxf(scale_log2 / row_factor, 1.17549435e-38f);
+}
+
 // Work of many unequal items laid out as one line of steps and cut into equal ranges,
 // one a block: sequence by sequence, KV head by KV head, item by item. Heads of a
 // sequence have the same items.
