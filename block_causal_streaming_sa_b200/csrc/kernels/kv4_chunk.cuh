@@ -34,7 +34,7 @@ struct ChunkShape {
   static constexpr int kBox = BN * 128;     // bytes of 64 columns of a tile
   static constexpr int NSTAGE = 4;          // K, V, K, V
   static constexpr int kThreads = 512;
-  static constexpr int kRegsSoftmax = 192, kRegsConvert = 88, kRegsIssue = 40;
+  static constexpr int kRegsSoftmax = 192, kRegsConvert = 72, kRegsIssue = 56;
   static_assert(2 * kRegsSoftmax + kRegsConvert + kRegsIssue <= 512, "launched at 128 each");
   static constexpr int kOffQ = 0;
   static constexpr int kOffKV = 2 * kTile;
@@ -65,6 +65,38 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t x, uint32_t y, ui
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z),
                "r"(w)
                : "memory");
+}
+
+// Products whose shared memory descriptors are given by their low words: the high word
+// (stride 1024 between groups of eight rows, version 1, 128-byte swizzle) is the same
+// for every tile here, and 64-bit descriptors kept ready would not fit the issuing
+// warp's registers.
+constexpr uint32_t kDescHi = 64u | 1u << 14 | 2u << 29;
+
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo_bytes) {
+  return ((addr >> 4) & 0x3FFFu) | (lbo_bytes >> 4) << 16;
+}
+
+__device__ __forceinline__ void umma_ss_lo(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                           bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)), "r"(kDescHi)
+      : "memory");
+}
+
+__device__ __forceinline__ void umma_ts_lo(uint32_t d, uint32_t a_tmem, uint32_t b, uint32_t idesc,
+                                           bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+      "mov.b64 db, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+      "r"(a_tmem), "r"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)), "r"(kDescHi)
+      : "memory");
 }
 
 // Key tiles that pair `pair` (query rows 256 pair ..) of sequence b goes through.
@@ -304,23 +336,21 @@ __global__ void __launch_bounds__(512, 1)
         return r;
       };
       auto issue_s = [&](int i, int sk) {
-        const uint32_t qa = sbase + S::kOffQ + i * S::kTile;
-        const uint32_t kb = sbase + S::kOffKV + sk * S::kTile;
+        const uint32_t qa = desc_lo(sbase + S::kOffQ + i * S::kTile, 16);
+        const uint32_t kb = desc_lo(sbase + S::kOffKV + sk * S::kTile, 16);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * S::kBox + (kk & 3) * 32;
-          ptx::umma_ss(tmem + S::col_s(i), ptx::smem_desc_sw128(qa + off, 16, 1024),
-                       ptx::smem_desc_sw128(kb + off, 16, 1024), S::kIdescQK, kk > 0 ? 1u : 0u);
+          const uint32_t off = ((kk >> 2) * S::kBox + (kk & 3) * 32) >> 4;
+          umma_ss_lo(tmem + i * 128, qa + off, kb + off, S::kIdescQK, kk > 0);
         }
         ptx::umma_commit(bar(S::SFULL(i)));
       };
       auto issue_pv = [&](int i, int sv, bool accumulate) {
-        const uint32_t vb = sbase + S::kOffKV + sv * S::kTile;
+        const uint32_t vb = desc_lo(sbase + S::kOffKV + sv * S::kTile, S::kBox);
 #pragma unroll
         for (int kk = 0; kk < S::BN / 16; ++kk)
-          ptx::umma_ts(tmem + S::col_o(i), tmem + S::col_p(i) + kk * 8,
-                       ptx::smem_desc_sw128(vb + kk * 16 * 128, S::kBox, 1024), S::kIdescPV,
-                       (accumulate || kk > 0) ? 1u : 0u);
+          umma_ts_lo(tmem + S::col_o(i), tmem + S::col_p(i) + kk * 8, vb + (kk * 16 * 128 >> 4),
+                     S::kIdescPV, accumulate || kk > 0);
       };
       while (ok && walk.next(p.line)) {
         const int n_rows = tokens_of(p.counts, walk.b, p.T) * p.group;
