@@ -1,58 +1,71 @@
 // Attention of many query rows over a 4-bit cache: chunks and prompts.
 //
-// Bound by the matrix and the exponential units: 4 D flop and one exponential per
-// (query row, cache row). The design is the chunk-cache attention's (two query tiles
-// of 128 rows ping-pong over every K / V tile, S and O in tensor memory, P written
-// over S), with these differences:
+// Bound by the matrix and exponential units and by what feeds them: 4 D flop and one
+// exponential per (query row, cache row). The design is the chunk-cache attention's
+// (query tiles of 128 rows ping-pong over every K / V tile, S and O in tensor memory,
+// P written over S), with these differences:
+//  * Two SMs work as a pair (cta_group::2, tiles of 256 query rows): each holds half of
+//    every K tile (64 of its 128 rows) and of every V tile (half the columns), which the
+//    tensor cores of both read. Alone, an SM's products read 192 KB of shared memory per
+//    step against the 2048 cycles they take, all that shared memory delivers, and
+//    the conversion's 64 KB came on top (3700 cycles a step measured); paired they read
+//    128 KB and write 32.
 //  * K and V arrive as codes. A warpgroup of its own reads them from global memory
 //    one tile ahead into registers, converts and scales them (exact in fp16) and
-//    stores them in the swizzled layout the products read, 350 instructions a thread
-//    and tile pair next to the ~2050 cycles of its four products. Converting on the
-//    fly reads 288 bytes a row and head instead of 512 + the 800 that a 16-bit copy
-//    made ahead would move, and needs no copy of the cache.
+//    stores them in the swizzled layout the products read. Converting on the fly reads
+//    288 bytes a row and head instead of the 512 + 800 that a 16-bit copy made ahead
+//    would move, and needs no copy of the cache.
 //  * Queries are staged once per call (kv4_stage_kernel): scaled to fp16 by a power
 //    of two per row and stored as the 128-row tiles' shared memory images, so a tile
-//    is one bulk copy whatever the tensor's strides are.
-//  * Work is one line of (query tile pair, key tile) steps cut into equal ranges, one
-//    a block, so neither causal masks, ragged lengths nor the last round leave SMs
-//    idle. A block writes whole pairs to O; of a pair that lies in several ranges
-//    each block leaves an fp32 partial result, at most two a block, which
+//    is one bulk copy whatever the tensor's strides are. They are double-buffered: the
+//    next item's arrive while this one is worked on.
+//  * Work is one line of (512 query rows, key tile) steps cut into equal ranges, one
+//    a pair of SMs, so neither causal masks, ragged lengths nor the last round leave
+//    SMs idle. A pair writes whole items to O; of an item that lies in several ranges
+//    each pair leaves an fp32 partial result, at most two a pair, which
 //    kv4_chunk_join_kernel merges in the order of the ranges.
-//  * Registers: 512 threads launched at 128; softmax warpgroups 192, conversion 88,
-//    the issuing warp's 40 (their sum is the launch's).
+//  * Registers: 512 threads launched at 128; softmax warpgroups 192, conversion 72,
+//    the issuing warpgroup 56 (their sum is the launch's).
 #pragma once
 
 #include "kv4_params.cuh"
 
 namespace sa {
 
+constexpr int kItemRows = 512;  // query rows of an item: two tiles of 256, each over two SMs
+
 template <int D>
 struct ChunkShape {
-  static constexpr int BM = 128, BN = 128;
-  static constexpr int KBLK = D / 64;       // 128-byte swizzle atoms of a row
-  static constexpr int kTile = BM * D * 2;  // bytes of a Q, K or V tile
-  static constexpr int kBox = BN * 128;     // bytes of 64 columns of a tile
+  static constexpr int BN = 128;            // cache rows of a key tile
+  static constexpr int kTile = 128 * D * 2; // bytes of a query tile's rows in one SM
+  static constexpr int kBox = 128 * 128;    // bytes of 64 columns of 128 rows
+  static constexpr int kHalf = 128 * D;     // bytes of half a K or V tile
   static constexpr int NSTAGE = 4;          // K, V, K, V
   static constexpr int kThreads = 512;
   static constexpr int kRegsSoftmax = 192, kRegsConvert = 72, kRegsIssue = 56;
   static_assert(2 * kRegsSoftmax + kRegsConvert + kRegsIssue <= 512, "launched at 128 each");
-  static constexpr int kOffQ = 0;
-  static constexpr int kOffKV = 2 * kTile;
-  static constexpr int kOffBar = kOffKV + NSTAGE * kTile;
+  static constexpr int kOffQ = 0;           // [buffer][tile]
+  static constexpr int kOffKV = 4 * kTile;
+  static constexpr int kOffBar = kOffKV + NSTAGE * kHalf;
   static constexpr int kSmem = kOffBar + 256 + 1024;  // + alignment slack
   static constexpr int kTmemCols = 512;
-  static constexpr uint32_t kIdescQK = ptx::idesc_f32acc(BM, BN, 0, 0);  // fp16
-  static constexpr uint32_t kIdescPV = ptx::idesc_f32acc(BM, D, 0, 1);   // fp16, V MN-major
+  static constexpr uint32_t kIdescQK = ptx::idesc_f32acc(256, BN, 0, 0);  // fp16
+  static constexpr uint32_t kIdescPV = ptx::idesc_f32acc(256, D, 0, 1);   // fp16, V MN-major
   __host__ __device__ static constexpr int col_s(int i) { return i * 128; }
   __host__ __device__ static constexpr int col_p(int i) { return i * 128 + 64; }
   __host__ __device__ static constexpr int col_o(int i) { return 256 + i * D; }
-  __host__ __device__ static constexpr int FULL(int s) { return s; }
+  // Barriers: the leader's (block 0 of the pair) collect arrivals of both blocks, the
+  // others are each block's own.
+  __host__ __device__ static constexpr int FULL(int s) { return s; }            // leader
   __host__ __device__ static constexpr int EMPTY(int s) { return NSTAGE + s; }
   __host__ __device__ static constexpr int SFULL(int i) { return 2 * NSTAGE + i; }
-  __host__ __device__ static constexpr int PFULL(int i) { return 2 * NSTAGE + 2 + i; }
+  __host__ __device__ static constexpr int PFULL(int i) { return 2 * NSTAGE + 2 + i; }  // leader
   __host__ __device__ static constexpr int OFINAL(int i) { return 2 * NSTAGE + 4 + i; }
-  __host__ __device__ static constexpr int QLOAD(int i) { return 2 * NSTAGE + 6 + i; }
-  __host__ __device__ static constexpr int DRAIN() { return 2 * NSTAGE + 8; }
+  __host__ __device__ static constexpr int QLOAD(int q) { return 2 * NSTAGE + 6 + q; }
+  __host__ __device__ static constexpr int QREADY(int q) { return 2 * NSTAGE + 8 + q; }  // leader
+  __host__ __device__ static constexpr int QEMPTY(int q) { return 2 * NSTAGE + 10 + q; }
+  __host__ __device__ static constexpr int DRAIN() { return 2 * NSTAGE + 12; }
+  static_assert(kSmem <= 232448, "shared memory");
 };
 
 // Offset of 16-byte piece c of row r in a 128-byte-swizzled K-major tile of 128 rows.
@@ -67,43 +80,96 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t x, uint32_t y, ui
                : "memory");
 }
 
-// Products whose shared memory descriptors are given by their low words: the high word
-// (stride 1024 between groups of eight rows, version 1, 128-byte swizzle) is the same
-// for every tile here, and 64-bit descriptors kept ready would not fit the issuing
-// warp's registers.
-constexpr uint32_t kDescHi = 64u | 1u << 14 | 2u << 29;
+// Products of a pair of SMs. Shared memory descriptors are given by their low words:
+// the high word (stride between groups of eight rows, version 1, swizzle) is the
+// same for all tiles of a kind, and 64-bit descriptors kept ready would not fit the
+// issuing warp's registers.
+constexpr uint32_t kDescHi128 = 64u | 1u << 14 | 2u << 29;  // 1024 bytes, 128-byte swizzle
+constexpr uint32_t kDescHi64 = 32u | 1u << 14 | 4u << 29;   // 512 bytes, 64-byte swizzle
 
 __device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo_bytes) {
   return ((addr >> 4) & 0x3FFFu) | (lbo_bytes >> 4) << 16;
 }
 
-__device__ __forceinline__ void umma_ss_lo(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
-                                           bool accumulate) {
+__device__ __forceinline__ void umma2_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                         bool accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
       "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "r"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)), "r"(kDescHi)
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)), "r"(kDescHi128)
       : "memory");
 }
 
-__device__ __forceinline__ void umma_ts_lo(uint32_t d, uint32_t a_tmem, uint32_t b, uint32_t idesc,
-                                           bool accumulate) {
+__device__ __forceinline__ void umma2_ts(uint32_t d, uint32_t a_tmem, uint32_t b, uint32_t b_hi,
+                                         uint32_t idesc, bool accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
       "mov.b64 db, {%2, %5};\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
-      "r"(a_tmem), "r"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)), "r"(kDescHi)
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+      "r"(a_tmem), "r"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)), "r"(b_hi)
       : "memory");
 }
 
-// Key tiles that pair `pair` (query rows 256 pair ..) of sequence b goes through.
-__device__ __forceinline__ int pair_tiles(const Kv4AttendParams& p, int held, int n_tok, int pair) {
+// Arrive on this barrier of both blocks when all earlier products have finished.
+__device__ __forceinline__ void umma2_commit(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;" ::"r"(bar),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+
+// The leader's copy of a barrier, and an arrival on it from either block.
+__device__ __forceinline__ uint32_t leader_addr(uint32_t addr) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+  return r;
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+               : "memory");
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Bounded wait on a barrier that the other block may arrive on.
+__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity,
+                                             volatile int* abort_flag, unsigned* status) {
+  auto done = [&]() {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+  };
+  if (done()) return true;
+  const long long t0 = clock64();
+  while (true) {
+    if (done()) return true;
+    if (*abort_flag) return false;
+    if (clock64() - t0 > ptx::kWaitCycles) {
+      *abort_flag = 1;
+      atomicOr(status, kDevErrTimeout);
+      return false;
+    }
+  }
+}
+
+// Key tiles that item `item` (query rows 512 item ..) of sequence b goes through.
+__device__ __forceinline__ int item_tiles(const Kv4AttendParams& p, int held, int n_tok, int item) {
   const int n_rows = n_tok * p.group;
-  if (256 * pair >= n_rows) return 0;
-  const int last = min(256 * pair + 256, n_rows) - 1;
+  if (kItemRows * item >= n_rows) return 0;
+  const int last = min(kItemRows * (item + 1), n_rows) - 1;
   return (rows_seen(p, held, n_tok, last / p.group) + 127) / 128;
 }
 
@@ -132,7 +198,7 @@ __global__ void __launch_bounds__(256)
       lay_line(p.line, c.B, c.H, [&](int b, int i) {
         const int n_tok = tokens_of(p.counts, b, p.T);
         if (i == 0) check_order(p, b, n_tok);
-        return pair_tiles(p, rows_held(c, b), n_tok, i);
+        return item_tiles(p, rows_held(c, b), n_tok, i);
       });
     } else {
       lay_line(p.weight_line, c.B, c.H, [&](int b, int i) {
@@ -146,7 +212,7 @@ __global__ void __launch_bounds__(256)
   const int held = rows_held(c, b), n_tok = tokens_of(p.counts, b, p.T);
   const int n_rows = n_tok * p.group;
   if (tile * 128 >= n_rows) return;
-  const bool empty = pair_tiles(p, held, n_tok, tile / 2) == 0;  // no block goes there
+  const bool empty = item_tiles(p, held, n_tok, tile * 128 / kItemRows) == 0;  // no block goes there
   const size_t tile_id = (static_cast<size_t>(b) * c.H + h) * p.q_tiles + tile;
   uint8_t* dst = p.q_img + tile_id * (128 * D * 2);
   for (int i = threadIdx.x; i < 128 * C; i += 256) {
@@ -188,22 +254,23 @@ __global__ void __launch_bounds__(256)
 // own so that its registers do not add to the score loop's.
 template <int D, int kDtype>
 __device__ __noinline__ void chunk_epilogue(const Kv4AttendParams& p, uint32_t tO, float m,
-                                            float lsum, bool whole, size_t slot, int i, int r,
-                                            int b, int h, int row, int n_rows) {
+                                            float lsum, bool whole, size_t slot, int b, int h,
+                                            int row, int n_rows) {
   if (!whole) {
-    float4* dst = reinterpret_cast<float4*>(p.part_o) + slot * (D / 4) * 256 + i * 128 + r;
+    const int r = row % kItemRows;
+    float4* dst = reinterpret_cast<float4*>(p.part_o) + slot * (D / 4) * kItemRows + r;
 #pragma unroll 1
     for (int j = 0; j < D / 32; ++j) {
       uint32_t o[32];
       ptx::tmem_ld32(tO + j * 32, o);
       ptx::tmem_wait_ld();
 #pragma unroll
-      for (int k = 0; k < 32; k += 4)  // [D / 4][256 rows][4]: a warp's stores are contiguous
-        dst[static_cast<size_t>(j * 8 + k / 4) * 256] =
+      for (int k = 0; k < 32; k += 4)  // [D / 4][512 rows][4]: a warp's stores are contiguous
+        dst[static_cast<size_t>(j * 8 + k / 4) * kItemRows] =
             make_float4(__uint_as_float(o[k]), __uint_as_float(o[k + 1]),
                         __uint_as_float(o[k + 2]), __uint_as_float(o[k + 3]));
     }
-    p.part_ml[slot * 256 + i * 128 + r] = make_float2(m, lsum);
+    p.part_ml[slot * kItemRows + r] = make_float2(m, lsum);
     return;
   }
   const float inv = lsum == 0.f ? 0.f : 1.f / lsum;  // NaN stays NaN
@@ -232,36 +299,36 @@ __device__ __noinline__ void chunk_epilogue(const Kv4AttendParams& p, uint32_t t
   }
 }
 
-// Codes of a thread's part of one K or V tile, read ahead: 16-byte pieces (32 codes),
-// piece i * 128 + thread of the tile's 128 * D / 32, with their two scales.
-template <int D>
+// Codes of a thread's part of a tile, read ahead: 16-byte pieces (32 codes), piece
+// i * 128 + thread of `P` a row, with their two scales.
+template <int N>
 struct ConvertRegs {
-  static constexpr int N = D / 32;
   uint4 w[N];
   uint32_t sc[N];
 };
 
-template <int D>
-__device__ __forceinline__ void convert_load(ConvertRegs<D>& x, const uint8_t* codes,
-                                             const uint8_t* scales, size_t row0, int tid) {
-  constexpr int P = D / 32;  // pieces of a row
-  const uint4* src = reinterpret_cast<const uint4*>(codes + row0 * (D / 2));
-  const uint16_t* sc = reinterpret_cast<const uint16_t*>(scales + row0 * (D / 16));
+// Pieces piece0 .. piece0 + P - 1 of rows row0 ..
+template <int D, int P, int N>
+__device__ __forceinline__ void convert_load(ConvertRegs<N>& x, const uint8_t* codes,
+                                             const uint8_t* scales, size_t row0, int piece0,
+                                             int tid) {
+  const uint4* src = reinterpret_cast<const uint4*>(codes + row0 * (D / 2)) + piece0;
+  const uint16_t* sc = reinterpret_cast<const uint16_t*>(scales + row0 * (D / 16)) + piece0;
 #pragma unroll
-  for (int i = 0; i < P; ++i) {
-    x.w[i] = __ldg(src + i * 128 + tid);
-    x.sc[i] = __ldg(sc + i * 128 + tid);
+  for (int i = 0; i < N; ++i) {
+    const int row = (i * 128 + tid) / P, piece = (i * 128 + tid) % P;
+    x.w[i] = __ldg(src + row * (D / 32) + piece);
+    x.sc[i] = __ldg(sc + row * (D / 32) + piece);
   }
 }
 
-// Into the swizzled tile; rows from `valid` on become zeros (what lies there may be
-// anything, and a scale may be NaN).
-template <int D>
-__device__ __forceinline__ void convert_store(const ConvertRegs<D>& x, uint32_t tile, int tid,
-                                              int valid) {
-  constexpr int P = D / 32;
+// Into a tile in shared memory, `offset(row, 16-byte piece)` from `tile`; rows from
+// `valid` on become zeros (what lies there may be anything, and a scale may be NaN).
+template <int P, int N, typename F>
+__device__ __forceinline__ void convert_store(const ConvertRegs<N>& x, uint32_t tile, int tid,
+                                              int valid, F offset) {
 #pragma unroll
-  for (int i = 0; i < P; ++i) {
+  for (int i = 0; i < N; ++i) {
     const int row = (i * 128 + tid) / P, piece = (i * 128 + tid) % P;
     const uint32_t bytes = row < valid ? x.sc[i] : 0u;
     const uint32_t s0 = scale_f16x2(bytes & 255u), s1 = scale_f16x2(bytes >> 8);
@@ -271,64 +338,78 @@ __device__ __forceinline__ void convert_store(const ConvertRegs<D>& x, uint32_t 
       uint32_t h[4];
       codes_to_f16(w[j], h);
       const uint32_t s = j < 2 ? s0 : s1;
-      sts128(tile + tile_offset(row, piece * 4 + j), mul_f16x2(h[0], s), mul_f16x2(h[1], s),
+      sts128(tile + offset(row, piece * 4 + j), mul_f16x2(h[0], s), mul_f16x2(h[1], s),
              mul_f16x2(h[2], s), mul_f16x2(h[3], s));
     }
   }
 }
 
 template <int D, int kDtype>
-__global__ void __launch_bounds__(512, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(512, 1)
     kv4_chunk_kernel(const __grid_constant__ Kv4AttendParams p) {
   using S = ChunkShape<D>;
   extern __shared__ uint8_t smem_raw[];
   const Kv4& c = p.c;
   const uint32_t raw = ptx::smem_addr(smem_raw);
   uint8_t* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
-  const uint32_t sbase = ptx::smem_addr(smem);
+  const uint32_t sbase = ptx::smem_addr(smem);  // the same offset in both blocks
   auto bar = [&](int i) { return sbase + S::kOffBar + 8u * static_cast<uint32_t>(i); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kOffBar + 240);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kOffBar + 248);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = blockIdx.x & 1;  // 0: the leader, which issues the products
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::NSTAGE; ++s) {
-      ptx::mbar_init(bar(S::FULL(s)), 4);  // the four converting warps
+      ptx::mbar_init(bar(S::FULL(s)), 8);  // four converting warps of each block
       ptx::mbar_init(bar(S::EMPTY(s)), 1);
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(bar(S::SFULL(i)), 1);
-      ptx::mbar_init(bar(S::PFULL(i)), 128);
+      ptx::mbar_init(bar(S::PFULL(i)), 8);  // four warps of each block
       ptx::mbar_init(bar(S::OFINAL(i)), 1);
       ptx::mbar_init(bar(S::QLOAD(i)), 1);
+      ptx::mbar_init(bar(S::QREADY(i)), 2);
+      ptx::mbar_init(bar(S::QEMPTY(i)), 1);
     }
     ptx::mbar_init(bar(S::DRAIN()), 1);
     *abort_flag = 0;
     ptx::fence_mbar_init();
   }
   if (warp == 12) {
-    ptx::tmem_alloc(ptx::smem_addr(tmem_slot), S::kTmemCols);
-    ptx::tmem_relinquish();
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     ptx::smem_addr(tmem_slot)),
+                 "r"(S::kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   ptx::tc_fence_before();
   __syncthreads();
+  cluster_sync();  // both blocks' barriers are there
   ptx::tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
   asm volatile("griddepcontrol.wait;" ::: "memory");  // staged queries and schedule
 
-  LineWalk walk = line_range(p.line, c.B);
+  LineWalk walk = line_range(p.line, c.B, pair, pairs);
+  auto wait = [&](int which, uint32_t parity) {
+    return wait_cluster(bar(which), parity, abort_flag, c.status);
+  };
+  // Tiles of 256 query rows of the walk's item: 1 or 2.
+  auto item_halves = [&]() {
+    return tokens_of(p.counts, walk.b, p.T) * p.group > walk.item * kItemRows + 256 ? 2 : 1;
+  };
 
   if (warp >= 12) {
     ptx::setmaxnreg_dec<S::kRegsIssue>();
-    if (warp == 12 && lane == 0) {
-      // ------------------------------------------------------------ MMA issuer
+    if (warp == 12 && lane == 0 && rank == 0) {
+      // ------------------------------------------------------------ MMA issuer (leader)
       int stage = 0;
-      uint32_t phase = 0, pf_phase[2] = {0u, 0u};
-      uint32_t q_units[2] = {0u, 0u};  // pairs so far that used query tile i
+      uint32_t phase = 0, pf_phase[2] = {0u, 0u}, item = 0;
       bool ok = true;
       auto take = [&](int& s_out) -> bool {
         s_out = stage;
-        const bool r = ptx::mbar_wait(bar(S::FULL(stage)), phase, abort_flag, c.status);
+        const bool r = wait(S::FULL(stage), phase);
         if (++stage == S::NSTAGE) {
           stage = 0;
           phase ^= 1u;
@@ -336,120 +417,138 @@ __global__ void __launch_bounds__(512, 1)
         return r;
       };
       auto issue_s = [&](int i, int sk) {
-        const uint32_t qa = desc_lo(sbase + S::kOffQ + i * S::kTile, 16);
-        const uint32_t kb = desc_lo(sbase + S::kOffKV + sk * S::kTile, 16);
+        const uint32_t qa = desc_lo(sbase + S::kOffQ + ((item & 1) * 2 + i) * S::kTile, 16);
+        const uint32_t kb = desc_lo(sbase + S::kOffKV + sk * S::kHalf, 16);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = ((kk >> 2) * S::kBox + (kk & 3) * 32) >> 4;
-          umma_ss_lo(tmem + i * 128, qa + off, kb + off, S::kIdescQK, kk > 0);
-        }
-        ptx::umma_commit(bar(S::SFULL(i)));
+        for (int kk = 0; kk < D / 16; ++kk)  // 64 columns: a box of 128 (Q) or 64 (K) rows
+          umma2_ss(tmem + i * 128, qa + (((kk >> 2) * S::kBox + (kk & 3) * 32) >> 4),
+                   kb + (((kk >> 2) * (S::kBox / 2) + (kk & 3) * 32) >> 4), S::kIdescQK, kk > 0);
+        umma2_commit(bar(S::SFULL(i)));
       };
       auto issue_pv = [&](int i, int sv, bool accumulate) {
-        const uint32_t vb = desc_lo(sbase + S::kOffKV + sv * S::kTile, S::kBox);
+        // D / 2 columns of V a block: rows of 128 (D 64: 64) bytes
+        const uint32_t vb = desc_lo(sbase + S::kOffKV + sv * S::kHalf, 16);
 #pragma unroll
         for (int kk = 0; kk < S::BN / 16; ++kk)
-          umma_ts_lo(tmem + S::col_o(i), tmem + S::col_p(i) + kk * 8, vb + (kk * 16 * 128 >> 4),
-                     S::kIdescPV, accumulate || kk > 0);
+          umma2_ts(tmem + S::col_o(i), tmem + S::col_p(i) + kk * 8, vb + (kk * 16 * D >> 4),
+                   D == 128 ? kDescHi128 : kDescHi64, S::kIdescPV, accumulate || kk > 0);
       };
       while (ok && walk.next(p.line)) {
-        const int n_rows = tokens_of(p.counts, walk.b, p.T) * p.group;
-        const int tiles = n_rows > walk.item * 256 + 128 ? 2 : 1;
-        const size_t tile_id =
-            (static_cast<size_t>(walk.b) * c.H + walk.h) * p.q_tiles + 2 * walk.item;
-        for (int i = 0; i < tiles && ok; ++i) {
-          // every product that read the previous tile is done once its O is final
-          if (q_units[i] > 0)
-            ok = ptx::mbar_wait(bar(S::OFINAL(i)), (q_units[i] - 1) & 1, abort_flag, c.status);
-          if (!ok) break;
-          ptx::mbar_arrive_expect_tx(bar(S::QLOAD(i)), S::kTile);
-          asm volatile(
-              "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, "
-              "[%3];" ::"r"(sbase + S::kOffQ + i * S::kTile),
-              "l"(p.q_img + (tile_id + i) * S::kTile), "r"(S::kTile), "r"(bar(S::QLOAD(i)))
-              : "memory");
-          ++q_units[i];
-        }
+        const int halves = item_halves();
         int sk = 0, sv = 0;
-        if (!ok || !take(sk)) {
-          ok = false;
-          break;
-        }
-        ptx::tc_fence_after();
-        for (int i = 0; i < tiles && ok; ++i) {
-          ok = ptx::mbar_wait(bar(S::QLOAD(i)), (q_units[i] - 1) & 1, abort_flag, c.status);
-          if (ok) issue_s(i, sk);
-        }
+        ok = wait(S::QREADY(item & 1), (item >> 1) & 1) && take(sk);
         if (!ok) break;
-        ptx::umma_commit(bar(S::EMPTY(sk)));
+        ptx::tc_fence_after();
+        for (int i = 0; i < halves; ++i) issue_s(i, sk);
+        umma2_commit(bar(S::EMPTY(sk)));
         for (int t = walk.t0; ok && t < walk.t1; ++t) {
           const bool more = t + 1 < walk.t1;
+          if (!more) umma2_commit(bar(S::QEMPTY(item & 1)));  // its last products are issued
           if (!take(sv) || (more && !take(sk))) {
             ok = false;
             break;
           }
-          ptx::tc_fence_after();
-          for (int i = 0; i < tiles; ++i) {
-            if (!ptx::mbar_wait(bar(S::PFULL(i)), pf_phase[i], abort_flag, c.status)) {
+          for (int i = 0; i < halves; ++i) {
+            if (!wait(S::PFULL(i), pf_phase[i])) {
               ok = false;
               break;
             }
             pf_phase[i] ^= 1u;
             ptx::tc_fence_after();
             issue_pv(i, sv, t > walk.t0);
-            if (i == tiles - 1) ptx::umma_commit(bar(S::EMPTY(sv)));
+            if (i == halves - 1) umma2_commit(bar(S::EMPTY(sv)));
             if (more)
               issue_s(i, sk);
             else
-              ptx::umma_commit(bar(S::OFINAL(i)));
+              umma2_commit(bar(S::OFINAL(i)));
           }
-          if (ok && more) ptx::umma_commit(bar(S::EMPTY(sk)));
+          if (ok && more) umma2_commit(bar(S::EMPTY(sk)));
         }
+        ++item;
       }
-      // every product finishes before tensor memory is released, and query copies land
-      // before the block can end (also after an abort)
+      umma2_commit(bar(S::DRAIN()));
+    }
+    if (warp == 13 && lane == 0) {
+      // ------------------------------------------------------------ query tiles
+      uint32_t item = 0;
+      bool ok = true;
       volatile int none = 0;
-      ptx::umma_commit(bar(S::DRAIN()));
-      ptx::mbar_wait(bar(S::DRAIN()), 0, &none, c.status);
-      for (int i = 0; i < 2; ++i)
-        if (q_units[i] > 0)
-          ptx::mbar_wait(bar(S::QLOAD(i)), (q_units[i] - 1) & 1, &none, c.status);
+      while (ok && walk.next(p.line)) {
+        const int q = item & 1, n_rows = tokens_of(p.counts, walk.b, p.T) * p.group;
+        ok = wait(S::QEMPTY(q), ((item >> 1) & 1) ^ 1u);
+        if (!ok) break;
+        // tiles rank and 2 + rank of the item's four, as far as they have rows
+        const int first = walk.item * 4 + rank;
+        const int tiles = n_rows > (first + 2) * 128 ? 2 : n_rows > first * 128 ? 1 : 0;
+        ptx::mbar_arrive_expect_tx(bar(S::QLOAD(q)), tiles * S::kTile);
+        for (int i = 0; i < tiles; ++i)
+          asm volatile(
+              "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, "
+              "[%3];" ::"r"(sbase + S::kOffQ + (q * 2 + i) * S::kTile),
+              "l"(p.q_img + ((static_cast<size_t>(walk.b) * c.H + walk.h) * p.q_tiles + first +
+                             2 * i) *
+                                S::kTile),
+              "r"(S::kTile), "r"(bar(S::QLOAD(q)))
+              : "memory");
+        // (also after an abort: the copies land before the block can end)
+        ok = ptx::mbar_wait(bar(S::QLOAD(q)), (item >> 1) & 1, &none, c.status);
+        ptx::fence_proxy_async_smem();
+        arrive_cluster(leader_addr(bar(S::QREADY(q))));
+        ++item;
+      }
     }
   } else if (warp >= 8) {
     ptx::setmaxnreg_dec<S::kRegsConvert>();
     // ------------------------------------------------------------ conversion
+    // K: rows 64 rank .. of the tile, all columns; V: all rows, columns D / 2 rank ..
+    constexpr int PK = D / 32, PV = D / 64, N = D / 64;
     const int tid = threadIdx.x - 256;
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
-    auto publish = [&](const ConvertRegs<D>& x, int valid) {
-      if (!__all_sync(~0u, ptx::mbar_wait(bar(S::EMPTY(stage)), phase ^ 1u, abort_flag,
-                                          c.status))) {
+    auto publish = [&](const ConvertRegs<N>& x, int valid, auto store) {
+      if (!__all_sync(~0u, wait(S::EMPTY(stage), phase ^ 1u))) {
         ok = false;
         return;
       }
-      convert_store<D>(x, sbase + S::kOffKV + stage * S::kTile, tid, valid);
+      store(x, sbase + S::kOffKV + stage * S::kHalf, valid);
       ptx::fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(bar(S::FULL(stage)));
+      if (lane == 0) arrive_cluster(leader_addr(bar(S::FULL(stage))));
       if (++stage == S::NSTAGE) {
         stage = 0;
         phase ^= 1u;
       }
     };
+    auto store_k = [&](const ConvertRegs<N>& x, uint32_t tile, int valid) {
+      convert_store<PK>(x, tile, tid, valid, [](int r, int c) {  // boxes of 64 rows
+        return static_cast<uint32_t>((c >> 3) * (64 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+      });
+    };
+    auto store_v = [&](const ConvertRegs<N>& x, uint32_t tile, int valid) {
+      convert_store<PV>(x, tile, tid, valid, [](int r, int c) {
+        if constexpr (D == 128) return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4));
+        return static_cast<uint32_t>(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+      });
+    };
     while (ok && walk.next(p.line)) {
       const int held = rows_held(c, walk.b);
       const size_t plane = (static_cast<size_t>(walk.b) * c.H + walk.h) * c.N;
-      ConvertRegs<D> kx, vx;
-      convert_load<D>(kx, c.k_codes, c.k_scales, plane + walk.t0 * 128, tid);
-      convert_load<D>(vx, c.v_codes, c.v_scales, plane + walk.t0 * 128, tid);
+      ConvertRegs<N> kx, vx;
+      auto load = [&](int t) {
+        convert_load<D, PK>(kx, c.k_codes, c.k_scales, plane + t * 128 + rank * 64, 0, tid);
+      };
+      auto load_v = [&](int t) {
+        convert_load<D, PV>(vx, c.v_codes, c.v_scales, plane + t * 128, rank * PV, tid);
+      };
+      load(walk.t0);
+      load_v(walk.t0);
       for (int t = walk.t0; ok && t < walk.t1; ++t) {
-        const size_t next = plane + (t + 1) * 128;
-        publish(kx, held - t * 128);
+        publish(kx, held - t * 128 - rank * 64, store_k);
         if (!ok) break;
-        if (t + 1 < walk.t1) convert_load<D>(kx, c.k_codes, c.k_scales, next, tid);
-        publish(vx, held - t * 128);
-        if (t + 1 < walk.t1) convert_load<D>(vx, c.v_codes, c.v_scales, next, tid);
+        if (t + 1 < walk.t1) load(t + 1);
+        publish(vx, held - t * 128, store_v);
+        if (t + 1 < walk.t1) load_v(t + 1);
       }
     }
   } else {
@@ -461,113 +560,128 @@ __global__ void __launch_bounds__(512, 1)
     const uint32_t t_lane = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t tS = tmem + t_lane + S::col_s(i);
     const uint32_t tO = tmem + t_lane + S::col_o(i);
-    uint32_t s_phase = 0, units = 0;
+    const uint32_t p_full = leader_addr(bar(S::PFULL(i)));
+    uint32_t s_phase = 0, items = 0;
     bool ok = true;
     while (ok && walk.next(p.line)) {
       const int held = rows_held(c, walk.b), n_tok = tokens_of(p.counts, walk.b, p.T);
       const int n_rows = n_tok * p.group;
-      if (i == 1 && n_rows <= walk.item * 256 + 128) continue;
-      const int row = walk.item * 256 + i * 128 + r;
+      if (i >= item_halves()) continue;
+      const int tile = walk.item * 4 + 2 * i + rank, row = tile * 128 + r;
+      const bool used = tile * 128 < n_rows;  // else this block's rows are not there
       const int end = row < n_rows ? rows_seen(p, held, n_tok, row / p.group) : held;
-      const float sl =
-          p.row_scale[((static_cast<size_t>(walk.b) * c.H + walk.h) * p.q_tiles) * 128 + row];
+      const float sl = used ? p.row_scale[((static_cast<size_t>(walk.b) * c.H + walk.h) *
+                                           p.q_tiles) * 128 + row]
+                            : 0.f;
       float m = -INFINITY, lsum = 0.f;
       for (int t = walk.t0; t < walk.t1; ++t) {
-        if (!__all_sync(~0u, ptx::mbar_wait(bar(S::SFULL(i)), s_phase, abort_flag, c.status))) {
+        if (!__all_sync(~0u, wait(S::SFULL(i), s_phase))) {
           ok = false;
           break;
         }
         s_phase ^= 1u;
         ptx::tc_fence_after();
-        uint32_t sr[4][32];
+        if (used) {
+          uint32_t sr[4][32];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) ptx::tmem_ld32(tS + j * 32, sr[j]);
-        ptx::tmem_wait_ld();
-        const int hi = end - t * 128;
-        if (hi < 128) {
+          for (int j = 0; j < 4; ++j) ptx::tmem_ld32(tS + j * 32, sr[j]);
+          ptx::tmem_wait_ld();
+          const int hi = end - t * 128;
+          if (hi < 128) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (j * 32 + k >= hi) sr[j][k] = __float_as_uint(-INFINITY);
+          }
+          float mx8[8];
+#pragma unroll
+          for (int a = 0; a < 8; ++a) mx8[a] = __uint_as_float(sr[0][a]);
 #pragma unroll
           for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (j * 32 + k >= hi) sr[j][k] = __float_as_uint(-INFINITY);
-        }
-        float mx8[8];
-#pragma unroll
-        for (int a = 0; a < 8; ++a) mx8[a] = __uint_as_float(sr[0][a]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int k = 0; k < 32; k += 2)
-            if (j > 0 || k >= 8)
-              mx8[(k >> 1) & 7] = ptx::fmax3(mx8[(k >> 1) & 7], __uint_as_float(sr[j][k]),
-                                             __uint_as_float(sr[j][k + 1]));
-        const float mx = fmaxf(ptx::fmax3(mx8[0], mx8[1], mx8[2]),
-                               fmaxf(ptx::fmax3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
-        const float m_new = fmaxf(m, mx * sl);
-        const bool need = m_new > m + 8.0f;
-        float alpha = 1.f;
-        if (need) {
-          alpha = ptx::ex2(m - m_new);
-          m = m_new;
-        }
-        // a row can meet a tile wholly behind its last key before any it sees
-        const float nm = m == -INFINITY ? 0.f : -m;
-        float rs8[8];
-#pragma unroll
-        for (int a = 0; a < 8; ++a) rs8[a] = 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            float x0, x1;
-            ptx::ffma2(x0, x1, __uint_as_float(sr[j][2 * k]), __uint_as_float(sr[j][2 * k + 1]),
-                       sl, sl, nm, nm);
-            const float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1);
-            const int a = (k & 3) * 2;
-            ptx::fadd2(rs8[a], rs8[a + 1], rs8[a], rs8[a + 1], p0, p1);
-            pk[k] = pack2<SA_DTYPE_FP16>(p0, p1);
+            for (int k = 0; k < 32; k += 2)
+              if (j > 0 || k >= 8)
+                mx8[(k >> 1) & 7] = ptx::fmax3(mx8[(k >> 1) & 7], __uint_as_float(sr[j][k]),
+                                               __uint_as_float(sr[j][k + 1]));
+          const float mx = fmaxf(ptx::fmax3(mx8[0], mx8[1], mx8[2]),
+                                 fmaxf(ptx::fmax3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
+          const float m_new = fmaxf(m, mx * sl);
+          const bool need = m_new > m + 8.0f;
+          float alpha = 1.f;
+          if (need) {
+            alpha = ptx::ex2(m - m_new);
+            m = m_new;
           }
-          ptx::tmem_st16(tS + 64 + j * 16, pk);
-        }
-        lsum = lsum * alpha +
-               (((rs8[0] + rs8[1]) + (rs8[2] + rs8[3])) + ((rs8[4] + rs8[5]) + (rs8[6] + rs8[7])));
-        // the first tile's P V overwrote O; a later growth of the maximum rescales it
-        if (__any_sync(~0u, need && t > walk.t0)) {
+          // a row can meet a tile wholly behind its last key before any it sees
+          const float nm = m == -INFINITY ? 0.f : -m;
+          float rs8[8];
 #pragma unroll
-          for (int j = 0; j < D / 32; ++j) {
-            uint32_t o[32];
-            ptx::tmem_ld32(tO + j * 32, o);
-            ptx::tmem_wait_ld();
+          for (int a = 0; a < 8; ++a) rs8[a] = 0.f;
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-            ptx::tmem_st32(tO + j * 32, o);
+          for (int j = 0; j < 4; ++j) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              float x0, x1;
+              ptx::ffma2(x0, x1, __uint_as_float(sr[j][2 * k]), __uint_as_float(sr[j][2 * k + 1]),
+                         sl, sl, nm, nm);
+              const float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1);
+              const int a = (k & 3) * 2;
+              ptx::fadd2(rs8[a], rs8[a + 1], rs8[a], rs8[a + 1], p0, p1);
+              pk[k] = pack2<SA_DTYPE_FP16>(p0, p1);
+            }
+            ptx::tmem_st16(tS + 64 + j * 16, pk);
           }
+          lsum = lsum * alpha +
+                 (((rs8[0] + rs8[1]) + (rs8[2] + rs8[3])) + ((rs8[4] + rs8[5]) + (rs8[6] + rs8[7])));
+          // the first tile's P V overwrote O; a later growth of the maximum rescales it
+          if (__any_sync(~0u, need && t > walk.t0)) {
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j) {
+              uint32_t o[32];
+              ptx::tmem_ld32(tO + j * 32, o);
+              ptx::tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+              ptx::tmem_st32(tO + j * 32, o);
+            }
+          }
+          ptx::tmem_wait_st();
         }
-        ptx::tmem_wait_st();
         ptx::tc_fence_before();
-        ptx::mbar_arrive(bar(S::PFULL(i)));
+        __syncwarp();
+        if (lane == 0) arrive_cluster(p_full);
       }
       if (!ok) break;
-      if (!__all_sync(~0u, ptx::mbar_wait(bar(S::OFINAL(i)), units & 1, abort_flag, c.status)))
-        break;
-      ++units;
+      if (!__all_sync(~0u, wait(S::OFINAL(i), items & 1))) break;
+      ++items;
       ptx::tc_fence_after();
-      chunk_epilogue<D, kDtype>(p, tO, m, lsum, walk.t0 == 0 && walk.t1 == walk.n,
-                                partial_slot(blockIdx.x, walk.t0), i, r, walk.b, walk.h, row,
-                                n_rows);
+      if (used)
+        chunk_epilogue<D, kDtype>(p, tO, m, lsum, walk.t0 == 0 && walk.t1 == walk.n,
+                                  partial_slot(pair, walk.t0), walk.b, walk.h, row, n_rows);
       ptx::tc_fence_before();
     }
   }
 
+  // Every product has finished before either block gives up its memory.
   ptx::tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0) {
+    volatile int none = 0;
+    wait_cluster(bar(S::DRAIN()), 0, &none, c.status);
+  }
+  __syncthreads();
+  cluster_sync();
   ptx::tc_fence_after();
-  if (warp == 12) ptx::tmem_dealloc(tmem, S::kTmemCols);
+  if (warp == 12)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(S::kTmemCols)
+                 : "memory");
 }
 
-// Merge of the pairs that lie in several blocks' ranges, one boundary (blockIdx.x) and 32
-// of the 256 query rows (blockIdx.y) a block.
+// Merge of the items that lie in several ranges, one boundary (blockIdx.x) and 32 of the
+// 512 query rows (blockIdx.y) a block.
 template <int D, int kDtype>
 __global__ void __launch_bounds__(128)
     kv4_chunk_join_kernel(const __grid_constant__ Kv4AttendParams p, int blocks) {
@@ -579,10 +693,10 @@ __global__ void __launch_bounds__(128)
   const int n_tok = tokens_of(p.counts, w.b, p.T), n_rows = n_tok * p.group;
   // four threads a row, D / 4 values each: r = row in the pair
   const int r = blockIdx.y * 32 + (threadIdx.x & 31), part = threadIdx.x >> 5;
-  const int row = w.item * 256 + r;
+  const int row = w.item * kItemRows + r;
   if (row >= n_rows) return;
   float mx = -INFINITY;
-  for (int k = split.first; k <= split.last; ++k) mx = fmaxf(mx, p.part_ml[split.slot(k) * 256 + r].x);
+  for (int k = split.first; k <= split.last; ++k) mx = fmaxf(mx, p.part_ml[split.slot(k) * kItemRows + r].x);
   const float ref = mx == -INFINITY ? 0.f : mx;
   float sum = 0.f;
   constexpr int V = D / 16;  // float4 of a thread
@@ -591,14 +705,14 @@ __global__ void __launch_bounds__(128)
   for (int j = 0; j < V; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int k = split.first; k <= split.last; ++k) {
     const size_t slot = split.slot(k);
-    const float2 ml = p.part_ml[slot * 256 + r];
+    const float2 ml = p.part_ml[slot * kItemRows + r];
     const float a = ptx::ex2(ml.x - ref);
     sum += ml.y * a;
     const float4* src =
-        reinterpret_cast<const float4*>(p.part_o) + slot * (D / 4) * 256 + part * V * 256 + r;
+        reinterpret_cast<const float4*>(p.part_o) + slot * (D / 4) * kItemRows + part * V * kItemRows + r;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const float4 x = src[j * 256];
+      const float4 x = src[j * kItemRows];
       acc[j].x = fmaf(x.x, a, acc[j].x);
       acc[j].y = fmaf(x.y, a, acc[j].y);
       acc[j].z = fmaf(x.z, a, acc[j].z);

@@ -38,11 +38,11 @@ struct Kv4AttendParams {
   float* scores;   // [B][H][N][score_rows], base 2
   int score_rows;
   // many query rows (kv4_chunk.cuh, kv4_weights.cuh)
-  int q_tiles, pairs;    // tiles of 128 query rows per (sequence, KV head), and pairs of them
+  int q_tiles;           // tiles of 128 query rows per (sequence, KV head)
   uint8_t* q_img;        // [B][H][q_tiles] shared memory images of the fp16 query tiles
   float* row_scale;      // [B][H][q_tiles * 128]: score factor of a staged row
   float* row_nlse;       // the same: minus its base-2 log-sum-exp, -inf if it draws no weight
-  StepLine line;         // steps of the attention: pairs x key tiles
+  StepLine line;         // steps of the attention: items of 512 query rows x key tiles
   StepLine weight_line;  // steps of the weights: key tiles x query tiles
   float* part_w;         // [slot][128]: partial sums of weights
 };
@@ -151,11 +151,11 @@ __device__ __forceinline__ long long line_share(const StepLine& line, int B, int
   return (line.begin[B] + blocks - 1) / blocks;
 }
 
-// This block's range of the line.
-__device__ __forceinline__ LineWalk line_range(const StepLine& line, int B) {
-  const long long share = line_share(line, B, gridDim.x), total = line.begin[B];
+// Range `block` of `blocks` of the line.
+__device__ __forceinline__ LineWalk line_range(const StepLine& line, int B, int block, int blocks) {
+  const long long share = line_share(line, B, blocks), total = line.begin[B];
   LineWalk w;
-  w.start(min(blockIdx.x * share, total), min((blockIdx.x + 1) * share, total));
+  w.start(min(block * share, total), min((block + 1) * share, total));
   return w;
 }
 

@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(448, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the attention's log-sum-exps
 
-  LineWalk walk = line_range(p.weight_line, c.B);
+  LineWalk walk = line_range(p.weight_line, c.B, blockIdx.x, gridDim.x);
   auto wait = [&](int which, uint32_t parity) {
     return ptx::mbar_wait(bar(which), parity, abort_flag, c.status);
   };
@@ -159,11 +159,12 @@ __global__ void __launch_bounds__(448, 1)
       const int kb = unit & 1;
       const size_t row0 = (static_cast<size_t>(walk.b) * c.H + walk.h) * c.N +
                           static_cast<size_t>(walk.item) * 128;
-      ConvertRegs<D> x;
-      convert_load<D>(x, c.k_codes, c.k_scales, row0, tid);
+      constexpr int P = D / 32;
+      ConvertRegs<P> x;
+      convert_load<D, P>(x, c.k_codes, c.k_scales, row0, 0, tid);
       if (!__all_sync(~0u, wait(S::KEMPTY(kb), ((unit >> 1) & 1) ^ 1u))) break;
-      convert_store<D>(x, sbase + S::kOffK + kb * S::kTile, tid,
-                       rows_held(c, walk.b) - walk.item * 128);
+      convert_store<P>(x, sbase + S::kOffK + kb * S::kTile, tid,
+                       rows_held(c, walk.b) - walk.item * 128, tile_offset);
       ptx::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bar(S::KFULL(kb)));

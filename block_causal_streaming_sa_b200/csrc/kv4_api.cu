@@ -158,7 +158,7 @@ int check_heads(const sa_kv4_cache* c, int heads, int T) {
     return refuse(SA_ERR_INVALID_ARG, "heads must be a multiple of kv_heads");
   const long long rows = 1LL * (heads / c->kv_heads) * T;
   if (heads > kMaxGridYZ || rows > (1LL << 30) ||
-      (rows + 255) / 256 * (c->capacity / 128) > INT32_MAX ||
+      (rows + 127) / 128 * (c->capacity / 128) > INT32_MAX ||
       1LL * c->batch * c->kv_heads * (c->capacity / 32) > INT32_MAX / 4)
     return refuse(SA_ERR_UNSUPPORTED, "too many query rows");
   return SA_OK;
@@ -227,7 +227,7 @@ struct AttendPlan {
   long long blocks;  // of the decode kernel, at most
   size_t off_o, off_ml, off_scores;
   // many query rows: kv4_chunk.cuh
-  int q_tiles, pairs;
+  int q_tiles, items;
   size_t off_q, off_scale, off_nlse, off_begin[2], off_pre[2], off_w;
   size_t total;
 };
@@ -262,19 +262,20 @@ AttendPlan plan_attend(const sa_kv4_cache* c, int heads, int T, bool weights) {
       return at;
     };
     a.q_tiles = (rows + 127) / 128;
-    a.pairs = (a.q_tiles + 1) / 2;
+    a.items = (rows + sa::kItemRows - 1) / sa::kItemRows;
     const size_t q_rows = planes * a.q_tiles * 128;
     a.off_q = take(q_rows * D * 2);
     a.off_scale = take(q_rows * sizeof(float));
     a.off_nlse = take(q_rows * sizeof(float));
-    const int items[2] = {a.pairs, c->capacity / 128};
+    const int items[2] = {a.items, c->capacity / 128};
     for (int i = 0; i < (weights ? 2 : 1); ++i) {
       a.off_begin[i] = take((c->batch + 1) * sizeof(long long));
       a.off_pre[i] = take(static_cast<size_t>(c->batch) * (items[i] + 1) * sizeof(int));
     }
     if (weights) a.off_w = take(2ull * kMostSms * 128 * sizeof(float));
-    a.off_o = take(2ull * kMostSms * 256 * D * sizeof(float));
-    a.off_ml = take(2ull * kMostSms * 256 * sizeof(float2));
+    // two partial results of 512 rows a pair of SMs
+    a.off_o = take(1ull * kMostSms * sa::kItemRows * D * sizeof(float));
+    a.off_ml = take(1ull * kMostSms * sa::kItemRows * sizeof(float2));
   }
   a.total = off;
   return a;
@@ -320,10 +321,12 @@ bool launch_chunk(const sa::Kv4AttendParams& p, cudaStream_t s) {
   const int blocks = std::min(sm_count(), kMostSms);
   sa::kv4_stage_kernel<D, kDtype>
       <<<dim3(p.q_tiles + (p.add_weight ? 2 : 1), p.c.H, p.c.B), 256, 0, s>>>(p);
-  launch_after(sa::kv4_chunk_kernel<D, kDtype>, dim3(blocks), dim3(S::kThreads), S::kSmem, s, p);
-  if (blocks > 1)
-    launch_after(sa::kv4_chunk_join_kernel<D, kDtype>, dim3(blocks - 1, 8), dim3(128), 0, s, p,
-                 blocks);
+  const int pairs = std::max(blocks / 2, 1);
+  launch_after(sa::kv4_chunk_kernel<D, kDtype>, dim3(2 * pairs), dim3(S::kThreads), S::kSmem, s,
+               p);
+  if (pairs > 1)
+    launch_after(sa::kv4_chunk_join_kernel<D, kDtype>, dim3(pairs - 1, sa::kItemRows / 32),
+                 dim3(128), 0, s, p, pairs);
   if (!p.add_weight) return true;
   using W = sa::WeightShape<D>;
   if (!allow_smem<sa::kv4_weight_kernel<D>>(W::kSmem)) return false;
@@ -496,7 +499,6 @@ SA_API int sa_kv4_attend(const sa_kv4_cache* c, const sa_rows* Q, const sa_rows*
     return launched("attention");
   }
   p.q_tiles = plan.q_tiles;
-  p.pairs = plan.pairs;
   p.q_img = ws + plan.off_q;
   p.row_scale = reinterpret_cast<float*>(ws + plan.off_scale);
   p.row_nlse = reinterpret_cast<float*>(ws + plan.off_nlse);
@@ -505,7 +507,7 @@ SA_API int sa_kv4_attend(const sa_kv4_cache* c, const sa_rows* Q, const sa_rows*
     return sa::StepLine{reinterpret_cast<long long*>(ws + plan.off_begin[i]),
                         reinterpret_cast<int*>(ws + plan.off_pre[i]), items};
   };
-  p.line = line(0, plan.pairs);
+  p.line = line(0, plan.items);
   p.weight_line = line(1, p.c.N / 128);
   const bool ok = D == 128 ? (dtype == SA_DTYPE_FP16 ? launch_chunk<128, SA_DTYPE_FP16>(p, s)
                                                      : launch_chunk<128, SA_DTYPE_BF16>(p, s))
