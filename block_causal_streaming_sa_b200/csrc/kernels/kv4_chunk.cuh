@@ -28,10 +28,13 @@
 //    the issuing warpgroup 56 (their sum is the launch's).
 #pragma once
 
+#include <type_traits>
+
 #include "kv4_params.cuh"
 
 namespace sa {
 
+constexpr int kPolyPairs = 0;
 constexpr int kItemRows = 512;  // query rows of an item: two tiles of 256, each over two SMs
 
 template <int D>
@@ -122,15 +125,27 @@ __device__ __forceinline__ void umma2_commit(uint32_t bar) {
       : "memory");
 }
 
-// The leader's copy of a barrier, and an arrival on it from either block.
+// The leader's copy of a barrier, and an arrival on it from either block. What is handed
+// over stays on the arriving SM: its shared memory (written, then fenced for the
+// asynchronous proxy) and tensor memory (ordered by tcgen05.wait and the fence before
+// the arrival) are read by that SM's own tensor core. So the release is the block's
+// (the default); one for the cluster took ~1000 cycles, between every P and its product.
 __device__ __forceinline__ uint32_t leader_addr(uint32_t addr) {
   uint32_t r;
   asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
   return r;
 }
-__device__ __forceinline__ void arrive_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
-               : "memory");
+__device__ __forceinline__ void arrive_leader(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// True in one lane of the (whole) warp, the same one at every call.
+__device__ __forceinline__ bool ptx_elect() {
+  uint32_t is;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(is));
+  return is != 0;
 }
 
 __device__ __forceinline__ void cluster_sync() {
@@ -356,7 +371,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(512, 1)
   auto bar = [&](int i) { return sbase + S::kOffBar + 8u * static_cast<uint32_t>(i); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kOffBar + 240);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kOffBar + 248);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = blockIdx.x & 1;  // 0: the leader, which issues the products
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
@@ -402,71 +417,97 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(512, 1)
 
   if (warp >= 12) {
     ptx::setmaxnreg_dec<S::kRegsIssue>();
-    if (warp == 12 && lane == 0 && rank == 0) {
+    if (warp == 12 && rank == 0) {
       // ------------------------------------------------------------ MMA issuer (leader)
-      int stage = 0;
-      uint32_t phase = 0, pf_phase[2] = {0u, 0u}, item = 0;
+      // The whole warp goes through the loop, so that the compiler sees uniform values and
+      // keeps them in uniform registers, which the product instructions take their
+      // operands from; one lane issues. A single thread's loop had to move every
+      // operand there (92 cycles a product instead of the 64 it runs).
+      const bool issues = ptx_elect();
+      int stage = 0, item = 0;
+      uint32_t phase = 0, p_phase0 = 0, p_phase1 = 0;
       bool ok = true;
+      auto all_wait = [&](int which, uint32_t parity) {
+        return __all_sync(~0u, wait(which, parity)) != 0;
+      };
       auto take = [&](int& s_out) -> bool {
         s_out = stage;
-        const bool r = wait(S::FULL(stage), phase);
+        const bool r = all_wait(S::FULL(stage), phase);
         if (++stage == S::NSTAGE) {
           stage = 0;
           phase ^= 1u;
         }
         return r;
       };
-      auto issue_s = [&](int i, int sk) {
+      auto issue_s = [&](auto tile, int sk) {
+        constexpr int i = decltype(tile)::value;
         const uint32_t qa = desc_lo(sbase + S::kOffQ + ((item & 1) * 2 + i) * S::kTile, 16);
         const uint32_t kb = desc_lo(sbase + S::kOffKV + sk * S::kHalf, 16);
+        if (issues) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)  // 64 columns: a box of 128 (Q) or 64 (K) rows
-          umma2_ss(tmem + i * 128, qa + (((kk >> 2) * S::kBox + (kk & 3) * 32) >> 4),
-                   kb + (((kk >> 2) * (S::kBox / 2) + (kk & 3) * 32) >> 4), S::kIdescQK, kk > 0);
-        umma2_commit(bar(S::SFULL(i)));
+          for (int kk = 0; kk < D / 16; ++kk)  // 64 columns: a box of 128 (Q) or 64 (K) rows
+            umma2_ss(tmem + S::col_s(i), qa + (((kk >> 2) * S::kBox + (kk & 3) * 32) >> 4),
+                     kb + (((kk >> 2) * (S::kBox / 2) + (kk & 3) * 32) >> 4), S::kIdescQK,
+                     kk > 0);
+          umma2_commit(bar(S::SFULL(i)));
+        }
       };
-      auto issue_pv = [&](int i, int sv, bool accumulate) {
+      auto issue_pv = [&](auto tile, int sv, bool accumulate) {
+        constexpr int i = decltype(tile)::value;
         // D / 2 columns of V a block: rows of 128 (D 64: 64) bytes
         const uint32_t vb = desc_lo(sbase + S::kOffKV + sv * S::kHalf, 16);
+        if (issues) {
 #pragma unroll
-        for (int kk = 0; kk < S::BN / 16; ++kk)
-          umma2_ts(tmem + S::col_o(i), tmem + S::col_p(i) + kk * 8, vb + (kk * 16 * D >> 4),
-                   D == 128 ? kDescHi128 : kDescHi64, S::kIdescPV, accumulate || kk > 0);
+          for (int kk = 0; kk < S::BN / 16; ++kk)
+            umma2_ts(tmem + S::col_o(i), tmem + S::col_p(i) + kk * 8, vb + (kk * 16 * D >> 4),
+                     D == 128 ? kDescHi128 : kDescHi64, S::kIdescPV, accumulate || kk > 0);
+        }
       };
+      auto commit = [&](int which) {
+        if (issues) umma2_commit(bar(which));
+      };
+      constexpr std::integral_constant<int, 0> tile0;
+      constexpr std::integral_constant<int, 1> tile1;
       while (ok && walk.next(p.line)) {
-        const int halves = item_halves();
+        const bool two = item_halves() == 2;
+        const int t0 = __shfl_sync(~0u, walk.t0, 0), t1 = __shfl_sync(~0u, walk.t1, 0);
         int sk = 0, sv = 0;
-        ok = wait(S::QREADY(item & 1), (item >> 1) & 1) && take(sk);
+        ok = all_wait(S::QREADY(item & 1), (item >> 1) & 1) && take(sk);
         if (!ok) break;
         ptx::tc_fence_after();
-        for (int i = 0; i < halves; ++i) issue_s(i, sk);
-        umma2_commit(bar(S::EMPTY(sk)));
-        for (int t = walk.t0; ok && t < walk.t1; ++t) {
-          const bool more = t + 1 < walk.t1;
-          if (!more) umma2_commit(bar(S::QEMPTY(item & 1)));  // its last products are issued
-          if (!take(sv) || (more && !take(sk))) {
-            ok = false;
-            break;
-          }
-          for (int i = 0; i < halves; ++i) {
-            if (!wait(S::PFULL(i), pf_phase[i])) {
-              ok = false;
-              break;
-            }
-            pf_phase[i] ^= 1u;
+        issue_s(tile0, sk);
+        if (two) issue_s(tile1, sk);
+        commit(S::EMPTY(sk));
+        for (int t = t0; ok && t < t1; ++t) {
+          const bool more = t + 1 < t1;
+          if (!more) commit(S::QEMPTY(item & 1));  // its last products are issued
+          ok = take(sv) && (!more || take(sk)) && all_wait(S::PFULL(0), p_phase0);
+          if (!ok) break;
+          p_phase0 ^= 1u;
+          ptx::tc_fence_after();
+          issue_pv(tile0, sv, t > t0);
+          if (!two) commit(S::EMPTY(sv));
+          if (more)
+            issue_s(tile0, sk);
+          else
+            commit(S::OFINAL(0));
+          if (two) {
+            ok = all_wait(S::PFULL(1), p_phase1);
+            if (!ok) break;
+            p_phase1 ^= 1u;
             ptx::tc_fence_after();
-            issue_pv(i, sv, t > walk.t0);
-            if (i == halves - 1) umma2_commit(bar(S::EMPTY(sv)));
+            issue_pv(tile1, sv, t > t0);
+            commit(S::EMPTY(sv));
             if (more)
-              issue_s(i, sk);
+              issue_s(tile1, sk);
             else
-              umma2_commit(bar(S::OFINAL(i)));
+              commit(S::OFINAL(1));
           }
-          if (ok && more) umma2_commit(bar(S::EMPTY(sk)));
+          if (more) commit(S::EMPTY(sk));
         }
         ++item;
       }
-      umma2_commit(bar(S::DRAIN()));
+      commit(S::DRAIN());
     }
     if (warp == 13 && lane == 0) {
       // ------------------------------------------------------------ query tiles
@@ -493,7 +534,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(512, 1)
         // (also after an abort: the copies land before the block can end)
         ok = ptx::mbar_wait(bar(S::QLOAD(q)), (item >> 1) & 1, &none, c.status);
         ptx::fence_proxy_async_smem();
-        arrive_cluster(leader_addr(bar(S::QREADY(q))));
+        arrive_leader(leader_addr(bar(S::QREADY(q))));
         ++item;
       }
     }
@@ -514,7 +555,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(512, 1)
       store(x, sbase + S::kOffKV + stage * S::kHalf, valid);
       ptx::fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) arrive_cluster(leader_addr(bar(S::FULL(stage))));
+      if (lane == 0) arrive_leader(leader_addr(bar(S::FULL(stage))));
       if (++stage == S::NSTAGE) {
         stage = 0;
         phase ^= 1u;
@@ -626,7 +667,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(512, 1)
               float x0, x1;
               ptx::ffma2(x0, x1, __uint_as_float(sr[j][2 * k]), __uint_as_float(sr[j][2 * k + 1]),
                          sl, sl, nm, nm);
-              const float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1);
+              float p0, p1;
+              if ((k & 7) >= 8 - kPolyPairs) {
+                exp2_fma2(p0, p1, x0, x1);
+              } else {
+                p0 = ptx::ex2(x0);
+                p1 = ptx::ex2(x1);
+              }
               const int a = (k & 3) * 2;
               ptx::fadd2(rs8[a], rs8[a + 1], rs8[a], rs8[a + 1], p0, p1);
               pk[k] = pack2<SA_DTYPE_FP16>(p0, p1);
@@ -651,12 +698,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(512, 1)
         }
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_cluster(p_full);
+        if (lane == 0) arrive_leader(p_full);
       }
       if (!ok) break;
       if (!__all_sync(~0u, wait(S::OFINAL(i), items & 1))) break;
       ++items;
       ptx::tc_fence_after();
+      if (m == -INFINITY) lsum = 0.f;  // no key seen: what the polynomial left of 2^-inf
       if (used)
         chunk_epilogue<D, kDtype>(p, tO, m, lsum, walk.t0 == 0 && walk.t1 == walk.n,
                                   partial_slot(pair, walk.t0), walk.b, walk.h, row, n_rows);

@@ -6,6 +6,32 @@
 
 namespace sa {
 
+// 2^x of two values on the FMA and integer pipes, for a share of the exponentials that
+// the exponential unit alone would hold up: x = n + f, n = round(x), 2^f on [-1/2, 1/2]
+// by a degree-5 polynomial (minimax in relative error, 2.4e-7 evaluated in fp32;
+// fit_exp2_poly.py), n added to the exponent. Below -127 the result is zero but for
+// the last bits of a subnormal. Softmax statistics come from these values, hence a
+// polynomial as exact as the unit (2^-22).
+__device__ __forceinline__ void exp2_fma2(float& y0, float& y1, float x0, float x1) {
+  constexpr float kRound = 12582912.0f;  // 1.5 * 2^23
+  constexpr float c0 = 1.0000001192092896f, c1 = 0.6931469440460205f, c2 = 0.24022120237350464f;
+  constexpr float c3 = 0.05550713092088699f, c4 = 0.009675540961325169f;
+  constexpr float c5 = 0.0013276472454890609f;
+  x0 = fmaxf(x0, -127.0f);
+  x1 = fmaxf(x1, -127.0f);
+  float t0, t1, f0, f1, q0, q1;
+  ptx::fadd2(t0, t1, x0, x1, kRound, kRound);
+  ptx::fadd2(f0, f1, t0, t1, -kRound, -kRound);  // n
+  ptx::ffma2(f0, f1, f0, f1, -1.0f, -1.0f, x0, x1);
+  ptx::ffma2(q0, q1, f0, f1, c5, c5, c4, c4);
+  ptx::ffma2(q0, q1, q0, q1, f0, f1, c3, c3);
+  ptx::ffma2(q0, q1, q0, q1, f0, f1, c2, c2);
+  ptx::ffma2(q0, q1, q0, q1, f0, f1, c1, c1);
+  ptx::ffma2(q0, q1, q0, q1, f0, f1, c0, c0);
+  y0 = __int_as_float(__float_as_int(q0) + (__float_as_int(t0) << 23));
+  y1 = __int_as_float(__float_as_int(q1) + (__float_as_int(t1) << 23));
+}
+
 // What a staged row's scores are multiplied with. Kept above zero: a masked score is
 // -inf, and 0 * -inf is not.
 __device__ __forceinline__ float score_factor(const float scale_log2, float row_factor) {
