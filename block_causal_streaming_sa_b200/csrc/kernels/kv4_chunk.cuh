@@ -10,6 +10,12 @@
 //    step against the 2048 cycles they take, all that shared memory delivers, and
 //    the conversion's 64 KB came on top (3700 cycles a step measured); paired they read
 //    128 KB and write 32.
+//  * A key tile's scores come as two halves of 64 rows in the two halves of a query
+//    tile's 128 columns. Softmax goes through them one after the other and puts P where
+//    half a's scores were; the next tile's half a goes where half b's were as soon as
+//    they have been read, and its half b over P once P V is done. So there are always
+//    scores to work on: with whole tiles, a tile's softmax (2100 cycles) and its products
+//    (1280 with their latencies) took turns, 3400 a step where each pipe needs 2048.
 //  * K and V arrive as codes. A warpgroup of its own reads them from global memory
 //    one tile ahead into registers, converts and scales them (exact in fp16) and
 //    stores them in the swizzled layout the products read. Converting on the fly reads
@@ -34,7 +40,6 @@
 
 namespace sa {
 
-constexpr int kPolyPairs = 0;
 constexpr int kItemRows = 512;  // query rows of an item: two tiles of 256, each over two SMs
 
 template <int D>
@@ -43,7 +48,7 @@ struct ChunkShape {
   static constexpr int kTile = 128 * D * 2; // bytes of a query tile's rows in one SM
   static constexpr int kBox = 128 * 128;    // bytes of 64 columns of 128 rows
   static constexpr int kHalf = 128 * D;     // bytes of half a K or V tile
-  static constexpr int NSTAGE = 4;          // K, V, K, V
+  static constexpr int NSTAGE = 6;          // K0 K1 V0 K2 V1 ..: K runs one tile ahead
   static constexpr int kThreads = 512;
   static constexpr int kRegsSoftmax = 192, kRegsConvert = 72, kRegsIssue = 56;
   static_assert(2 * kRegsSoftmax + kRegsConvert + kRegsIssue <= 512, "launched at 128 each");
@@ -52,22 +57,25 @@ struct ChunkShape {
   static constexpr int kOffBar = kOffKV + NSTAGE * kHalf;
   static constexpr int kSmem = kOffBar + 256 + 1024;  // + alignment slack
   static constexpr int kTmemCols = 512;
-  static constexpr uint32_t kIdescQK = ptx::idesc_f32acc(256, BN, 0, 0);  // fp16
+  static constexpr uint32_t kIdescQK = ptx::idesc_f32acc(256, 64, 0, 0);  // fp16
   static constexpr uint32_t kIdescPV = ptx::idesc_f32acc(256, D, 0, 1);   // fp16, V MN-major
-  __host__ __device__ static constexpr int col_s(int i) { return i * 128; }
-  __host__ __device__ static constexpr int col_p(int i) { return i * 128 + 64; }
+  // Tensor memory: per query tile two 64-column halves for scores and P, and O.
+  __host__ __device__ static constexpr int col_x(int i, int half) { return i * 128 + half * 64; }
   __host__ __device__ static constexpr int col_o(int i) { return 256 + i * D; }
   // Barriers: the leader's (block 0 of the pair) collect arrivals of both blocks, the
   // others are each block's own.
-  __host__ __device__ static constexpr int FULL(int s) { return s; }            // leader
+  __host__ __device__ static constexpr int FULL(int s) { return s; }  // leader
   __host__ __device__ static constexpr int EMPTY(int s) { return NSTAGE + s; }
-  __host__ __device__ static constexpr int SFULL(int i) { return 2 * NSTAGE + i; }
-  __host__ __device__ static constexpr int PFULL(int i) { return 2 * NSTAGE + 2 + i; }  // leader
-  __host__ __device__ static constexpr int OFINAL(int i) { return 2 * NSTAGE + 4 + i; }
-  __host__ __device__ static constexpr int QLOAD(int q) { return 2 * NSTAGE + 6 + q; }
-  __host__ __device__ static constexpr int QREADY(int q) { return 2 * NSTAGE + 8 + q; }  // leader
-  __host__ __device__ static constexpr int QEMPTY(int q) { return 2 * NSTAGE + 10 + q; }
-  __host__ __device__ static constexpr int DRAIN() { return 2 * NSTAGE + 12; }
+  __host__ __device__ static constexpr int SA(int i) { return 2 * NSTAGE + i; }
+  __host__ __device__ static constexpr int SB(int i) { return 2 * NSTAGE + 2 + i; }
+  __host__ __device__ static constexpr int READ(int i) { return 2 * NSTAGE + 4 + i; }   // leader
+  __host__ __device__ static constexpr int PFULL(int i) { return 2 * NSTAGE + 6 + i; }  // leader
+  __host__ __device__ static constexpr int OFINAL(int i) { return 2 * NSTAGE + 8 + i; }
+  __host__ __device__ static constexpr int QLOAD(int q) { return 2 * NSTAGE + 10 + q; }
+  __host__ __device__ static constexpr int QREADY(int q) { return 2 * NSTAGE + 12 + q; }  // leader
+  __host__ __device__ static constexpr int QEMPTY(int q) { return 2 * NSTAGE + 14 + q; }
+  __host__ __device__ static constexpr int DRAIN() { return 2 * NSTAGE + 16; }
+  static_assert((2 * NSTAGE + 17) * 8 <= 240, "barrier area");
   static_assert(kSmem <= 232448, "shared memory");
 };
 
@@ -314,6 +322,35 @@ __device__ __noinline__ void chunk_epilogue(const Kv4AttendParams& p, uint32_t t
   }
 }
 
+// Rare steps of the softmax, functions of their own so that their registers do not add
+// to the score loop's: scale D columns of fp32, and 32 columns of fp16 pairs.
+template <int D>
+__device__ __noinline__ void chunk_scale_columns(uint32_t tO, float alpha) {
+#pragma unroll 1
+  for (int j = 0; j < D / 32; ++j) {
+    uint32_t o[32];
+    ptx::tmem_ld32(tO + j * 32, o);
+    ptx::tmem_wait_ld();
+#pragma unroll
+    for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+    ptx::tmem_st32(tO + j * 32, o);
+  }
+  ptx::tmem_wait_st();
+}
+
+__device__ __noinline__ void chunk_scale_p(uint32_t tP, float alpha) {
+  uint32_t v[32];
+  ptx::tmem_ld32(tP, v);
+  ptx::tmem_wait_ld();
+#pragma unroll
+  for (int k = 0; k < 32; ++k) {
+    const float2 f = unpack2<SA_DTYPE_FP16>(v[k]);
+    v[k] = pack2<SA_DTYPE_FP16>(f.x * alpha, f.y * alpha);
+  }
+  ptx::tmem_st32(tP, v);
+  ptx::tmem_wait_st();
+}
+
 // Codes of a thread's part of a tile, read ahead: 16-byte pieces (32 codes), piece
 // i * 128 + thread of `P` a row, with their two scales.
 template <int N>
@@ -322,30 +359,30 @@ struct ConvertRegs {
   uint32_t sc[N];
 };
 
-// Pieces piece0 .. piece0 + P - 1 of rows row0 ..
-template <int D, int P, int N>
+// Pieces piece0 .. piece0 + P - 1 of rows row0 + key(row).
+template <int D, int P, int N, typename F>
 __device__ __forceinline__ void convert_load(ConvertRegs<N>& x, const uint8_t* codes,
                                              const uint8_t* scales, size_t row0, int piece0,
-                                             int tid) {
+                                             int tid, F key) {
   const uint4* src = reinterpret_cast<const uint4*>(codes + row0 * (D / 2)) + piece0;
   const uint16_t* sc = reinterpret_cast<const uint16_t*>(scales + row0 * (D / 16)) + piece0;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const int row = (i * 128 + tid) / P, piece = (i * 128 + tid) % P;
-    x.w[i] = __ldg(src + row * (D / 32) + piece);
-    x.sc[i] = __ldg(sc + row * (D / 32) + piece);
+    x.w[i] = __ldg(src + key(row) * (D / 32) + piece);
+    x.sc[i] = __ldg(sc + key(row) * (D / 32) + piece);
   }
 }
 
-// Into a tile in shared memory, `offset(row, 16-byte piece)` from `tile`; rows from
-// `valid` on become zeros (what lies there may be anything, and a scale may be NaN).
-template <int P, int N, typename F>
+// Into a tile in shared memory, `offset(row, 16-byte piece)` from `tile`; cache rows
+// from `valid` on become zeros (what lies there may be anything, and a scale may be NaN).
+template <int P, int N, typename F, typename G>
 __device__ __forceinline__ void convert_store(const ConvertRegs<N>& x, uint32_t tile, int tid,
-                                              int valid, F offset) {
+                                              int valid, F key, G offset) {
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const int row = (i * 128 + tid) / P, piece = (i * 128 + tid) % P;
-    const uint32_t bytes = row < valid ? x.sc[i] : 0u;
+    const uint32_t bytes = key(row) < valid ? x.sc[i] : 0u;
     const uint32_t s0 = scale_f16x2(bytes & 255u), s1 = scale_f16x2(bytes >> 8);
     const uint32_t w[4] = {x.w[i].x, x.w[i].y, x.w[i].z, x.w[i].w};
 #pragma unroll
@@ -381,8 +418,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(512, 1)
       ptx::mbar_init(bar(S::EMPTY(s)), 1);
     }
     for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(bar(S::SFULL(i)), 1);
-      ptx::mbar_init(bar(S::PFULL(i)), 8);  // four warps of each block
+      ptx::mbar_init(bar(S::SA(i)), 1);
+      ptx::mbar_init(bar(S::SB(i)), 1);
+      ptx::mbar_init(bar(S::READ(i)), 8);  // four warps of each block
+      ptx::mbar_init(bar(S::PFULL(i)), 8);
       ptx::mbar_init(bar(S::OFINAL(i)), 1);
       ptx::mbar_init(bar(S::QLOAD(i)), 1);
       ptx::mbar_init(bar(S::QREADY(i)), 2);
@@ -425,7 +464,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(512, 1)
       // operand there (92 cycles a product instead of the 64 it runs).
       const bool issues = ptx_elect();
       int stage = 0, item = 0;
-      uint32_t phase = 0, p_phase0 = 0, p_phase1 = 0;
+      uint32_t phase = 0, sm_phase[2] = {0u, 0u};
       bool ok = true;
       auto all_wait = [&](int which, uint32_t parity) {
         return __all_sync(~0u, wait(which, parity)) != 0;
@@ -439,27 +478,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(512, 1)
         }
         return r;
       };
-      auto issue_s = [&](auto tile, int sk) {
+      // Scores of half `b` of a key tile (32 of each block's 64 rows) into half `x`.
+      auto issue_s = [&](auto tile, int sk, int b, int x) {
         constexpr int i = decltype(tile)::value;
         const uint32_t qa = desc_lo(sbase + S::kOffQ + ((item & 1) * 2 + i) * S::kTile, 16);
-        const uint32_t kb = desc_lo(sbase + S::kOffKV + sk * S::kHalf, 16);
+        const uint32_t kb = desc_lo(sbase + S::kOffKV + sk * S::kHalf + b * 32 * 128, 16);
         if (issues) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)  // 64 columns: a box of 128 (Q) or 64 (K) rows
-            umma2_ss(tmem + S::col_s(i), qa + (((kk >> 2) * S::kBox + (kk & 3) * 32) >> 4),
+            umma2_ss(tmem + S::col_x(i, 0) + x * 64,
+                     qa + (((kk >> 2) * S::kBox + (kk & 3) * 32) >> 4),
                      kb + (((kk >> 2) * (S::kBox / 2) + (kk & 3) * 32) >> 4), S::kIdescQK,
                      kk > 0);
-          umma2_commit(bar(S::SFULL(i)));
+          umma2_commit(bar(b == 0 ? S::SA(i) : S::SB(i)));
         }
       };
-      auto issue_pv = [&](auto tile, int sv, bool accumulate) {
+      auto issue_pv = [&](auto tile, int sv, int x, bool accumulate) {
         constexpr int i = decltype(tile)::value;
         // D / 2 columns of V a block: rows of 128 (D 64: 64) bytes
         const uint32_t vb = desc_lo(sbase + S::kOffKV + sv * S::kHalf, 16);
         if (issues) {
 #pragma unroll
           for (int kk = 0; kk < S::BN / 16; ++kk)
-            umma2_ts(tmem + S::col_o(i), tmem + S::col_p(i) + kk * 8, vb + (kk * 16 * D >> 4),
+            umma2_ts(tmem + S::col_o(i), tmem + S::col_x(i, 0) + x * 64 + kk * 8,
+                     vb + (kk * 16 * D >> 4),
                      D == 128 ? kDescHi128 : kDescHi64, S::kIdescPV, accumulate || kk > 0);
         }
       };
@@ -475,35 +517,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(512, 1)
         ok = all_wait(S::QREADY(item & 1), (item >> 1) & 1) && take(sk);
         if (!ok) break;
         ptx::tc_fence_after();
-        issue_s(tile0, sk);
-        if (two) issue_s(tile1, sk);
+        issue_s(tile0, sk, 0, 0);
+        issue_s(tile0, sk, 1, 1);
+        if (two) {
+          issue_s(tile1, sk, 0, 0);
+          issue_s(tile1, sk, 1, 1);
+        }
         commit(S::EMPTY(sk));
-        for (int t = t0; ok && t < t1; ++t) {
+        int x = 0;  // half of P (and of half a's scores) of this tile
+        for (int t = t0; ok && t < t1; ++t, x ^= 1) {
           const bool more = t + 1 < t1;
           if (!more) commit(S::QEMPTY(item & 1));  // its last products are issued
-          ok = take(sv) && (!more || take(sk)) && all_wait(S::PFULL(0), p_phase0);
-          if (!ok) break;
-          p_phase0 ^= 1u;
-          ptx::tc_fence_after();
-          issue_pv(tile0, sv, t > t0);
-          if (!two) commit(S::EMPTY(sv));
-          if (more)
-            issue_s(tile0, sk);
-          else
-            commit(S::OFINAL(0));
-          if (two) {
-            ok = all_wait(S::PFULL(1), p_phase1);
-            if (!ok) break;
-            p_phase1 ^= 1u;
+          ok = (!more || take(sk)) && take(sv);
+          // One query tile: half a of the next scores, P V, half b of the next scores.
+          auto step = [&](auto tile, bool last) {
+            constexpr int i = decltype(tile)::value;
+            ok = ok && all_wait(S::READ(i), sm_phase[i]);
+            if (!ok) return;
             ptx::tc_fence_after();
-            issue_pv(tile1, sv, t > t0);
-            commit(S::EMPTY(sv));
+            if (more) issue_s(tile, sk, 0, x ^ 1);
+            ok = all_wait(S::PFULL(i), sm_phase[i]);
+            if (!ok) return;
+            sm_phase[i] ^= 1u;
+            ptx::tc_fence_after();
+            issue_pv(tile, sv, x, t > t0);
+            if (last) commit(S::EMPTY(sv));
             if (more)
-              issue_s(tile1, sk);
+              issue_s(tile, sk, 1, x);
             else
-              commit(S::OFINAL(1));
-          }
-          if (more) commit(S::EMPTY(sk));
+              commit(S::OFINAL(i));
+          };
+          step(tile0, !two);
+          if (two) step(tile1, true);
+          if (ok && more) commit(S::EMPTY(sk));
         }
         ++item;
       }
@@ -541,7 +587,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(512, 1)
   } else if (warp >= 8) {
     ptx::setmaxnreg_dec<S::kRegsConvert>();
     // ------------------------------------------------------------ conversion
-    // K: rows 64 rank .. of the tile, all columns; V: all rows, columns D / 2 rank ..
+    // K: rows 32 rank .. of each half of the tile, all columns; V: all rows, columns
+    // D / 2 rank ..
     constexpr int PK = D / 32, PV = D / 64, N = D / 64;
     const int tid = threadIdx.x - 256;
     int stage = 0;
@@ -561,13 +608,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(512, 1)
         phase ^= 1u;
       }
     };
+    auto key_k = [&](int r) { return r + rank * 32 + (r & 32); };
+    auto key_v = [](int r) { return r; };
     auto store_k = [&](const ConvertRegs<N>& x, uint32_t tile, int valid) {
-      convert_store<PK>(x, tile, tid, valid, [](int r, int c) {  // boxes of 64 rows
+      convert_store<PK>(x, tile, tid, valid, key_k, [](int r, int c) {  // boxes of 64 rows
         return static_cast<uint32_t>((c >> 3) * (64 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
       });
     };
     auto store_v = [&](const ConvertRegs<N>& x, uint32_t tile, int valid) {
-      convert_store<PV>(x, tile, tid, valid, [](int r, int c) {
+      convert_store<PV>(x, tile, tid, valid, key_v, [](int r, int c) {
         if constexpr (D == 128) return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4));
         return static_cast<uint32_t>(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
       });
@@ -576,18 +625,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(512, 1)
       const int held = rows_held(c, walk.b);
       const size_t plane = (static_cast<size_t>(walk.b) * c.H + walk.h) * c.N;
       ConvertRegs<N> kx, vx;
-      auto load = [&](int t) {
-        convert_load<D, PK>(kx, c.k_codes, c.k_scales, plane + t * 128 + rank * 64, 0, tid);
+      auto load_k = [&](int t) {
+        convert_load<D, PK>(kx, c.k_codes, c.k_scales, plane + t * 128, 0, tid, key_k);
       };
       auto load_v = [&](int t) {
-        convert_load<D, PV>(vx, c.v_codes, c.v_scales, plane + t * 128, rank * PV, tid);
+        convert_load<D, PV>(vx, c.v_codes, c.v_scales, plane + t * 128, rank * PV, tid, key_v);
       };
-      load(walk.t0);
+      load_k(walk.t0);
       load_v(walk.t0);
+      publish(kx, held - walk.t0 * 128, store_k);
+      if (walk.t0 + 1 < walk.t1) load_k(walk.t0 + 1);
       for (int t = walk.t0; ok && t < walk.t1; ++t) {
-        publish(kx, held - t * 128 - rank * 64, store_k);
-        if (!ok) break;
-        if (t + 1 < walk.t1) load(t + 1);
+        if (t + 1 < walk.t1) {
+          publish(kx, held - (t + 1) * 128, store_k);
+          if (!ok) break;
+          if (t + 2 < walk.t1) load_k(t + 2);
+        }
         publish(vx, held - t * 128, store_v);
         if (t + 1 < walk.t1) load_v(t + 1);
       }
@@ -599,9 +652,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(512, 1)
     const int quarter = warp & 3;  // tensor memory lanes this warp may access
     const int r = quarter * 32 + lane;
     const uint32_t t_lane = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t tS = tmem + t_lane + S::col_s(i);
+    const uint32_t tX = tmem + t_lane + S::col_x(i, 0);
     const uint32_t tO = tmem + t_lane + S::col_o(i);
-    const uint32_t p_full = leader_addr(bar(S::PFULL(i)));
+    const uint32_t read = leader_addr(bar(S::READ(i))), p_full = leader_addr(bar(S::PFULL(i)));
     uint32_t s_phase = 0, items = 0;
     bool ok = true;
     while (ok && walk.next(p.line)) {
@@ -615,87 +668,115 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(512, 1)
                                            p.q_tiles) * 128 + row]
                             : 0.f;
       float m = -INFINITY, lsum = 0.f;
-      for (int t = walk.t0; t < walk.t1; ++t) {
-        if (!__all_sync(~0u, wait(S::SFULL(i), s_phase))) {
-          ok = false;
-          break;
-        }
-        s_phase ^= 1u;
-        ptx::tc_fence_after();
-        if (used) {
-          uint32_t sr[4][32];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) ptx::tmem_ld32(tS + j * 32, sr[j]);
+      for (int t = walk.t0, x = 0; t < walk.t1; ++t, x ^= 1) {
+        uint32_t sr[2][32];  // a half's scores
+        const uint32_t tA = tX + x * 64, tB = tX + (x ^ 1) * 64;  // a, then P; b
+        auto load = [&](int half, uint32_t from) {
+          ptx::tc_fence_after();
+          if (!used) return;
+          ptx::tmem_ld32(from, sr[0]);
+          ptx::tmem_ld32(from + 32, sr[1]);
           ptx::tmem_wait_ld();
-          const int hi = end - t * 128;
-          if (hi < 128) {
+          const int hi = end - t * 128 - half * 64;
+          if (hi < 64) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
               for (int k = 0; k < 32; ++k)
                 if (j * 32 + k >= hi) sr[j][k] = __float_as_uint(-INFINITY);
           }
-          float mx8[8];
+        };
+        auto row_max = [&]() {  // of the scaled scores
+          float mx[8];
 #pragma unroll
-          for (int a = 0; a < 8; ++a) mx8[a] = __uint_as_float(sr[0][a]);
+          for (int a = 0; a < 8; ++a) mx[a] = __uint_as_float(sr[0][a]);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+          for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int k = 0; k < 32; k += 2)
               if (j > 0 || k >= 8)
-                mx8[(k >> 1) & 7] = ptx::fmax3(mx8[(k >> 1) & 7], __uint_as_float(sr[j][k]),
-                                               __uint_as_float(sr[j][k + 1]));
-          const float mx = fmaxf(ptx::fmax3(mx8[0], mx8[1], mx8[2]),
-                                 fmaxf(ptx::fmax3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
-          const float m_new = fmaxf(m, mx * sl);
-          const bool need = m_new > m + 8.0f;
-          float alpha = 1.f;
-          if (need) {
-            alpha = ptx::ex2(m - m_new);
-            m = m_new;
-          }
-          // a row can meet a tile wholly behind its last key before any it sees
+                mx[(k >> 1) & 7] = ptx::fmax3(mx[(k >> 1) & 7], __uint_as_float(sr[j][k]),
+                                              __uint_as_float(sr[j][k + 1]));
+          return fmaxf(ptx::fmax3(mx[0], mx[1], mx[2]),
+                       fmaxf(ptx::fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]))) *
+                 sl;
+        };
+        // P = 2^(s * scale - m) of a half; returns the row's sum
+        auto exponentials = [&](uint32_t to) {
+          // a row can meet keys wholly behind its last one before any it sees
           const float nm = m == -INFINITY ? 0.f : -m;
-          float rs8[8];
+          float rs[8];
 #pragma unroll
-          for (int a = 0; a < 8; ++a) rs8[a] = 0.f;
+          for (int a = 0; a < 8; ++a) rs[a] = 0.f;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+          for (int j = 0; j < 2; ++j) {
             uint32_t pk[16];
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
               float x0, x1;
               ptx::ffma2(x0, x1, __uint_as_float(sr[j][2 * k]), __uint_as_float(sr[j][2 * k + 1]),
                          sl, sl, nm, nm);
-              float p0, p1;
-              if ((k & 7) >= 8 - kPolyPairs) {
-                exp2_fma2(p0, p1, x0, x1);
-              } else {
-                p0 = ptx::ex2(x0);
-                p1 = ptx::ex2(x1);
-              }
+              const float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1);
               const int a = (k & 3) * 2;
-              ptx::fadd2(rs8[a], rs8[a + 1], rs8[a], rs8[a + 1], p0, p1);
+              ptx::fadd2(rs[a], rs[a + 1], rs[a], rs[a + 1], p0, p1);
               pk[k] = pack2<SA_DTYPE_FP16>(p0, p1);
             }
-            ptx::tmem_st16(tS + 64 + j * 16, pk);
+            ptx::tmem_st16(to + j * 16, pk);
           }
-          lsum = lsum * alpha +
-                 (((rs8[0] + rs8[1]) + (rs8[2] + rs8[3])) + ((rs8[4] + rs8[5]) + (rs8[6] + rs8[7])));
-          // the first tile's P V overwrote O; a later growth of the maximum rescales it
-          if (__any_sync(~0u, need && t > walk.t0)) {
-#pragma unroll
-            for (int j = 0; j < D / 32; ++j) {
-              uint32_t o[32];
-              ptx::tmem_ld32(tO + j * 32, o);
-              ptx::tmem_wait_ld();
-#pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-              ptx::tmem_st32(tO + j * 32, o);
-            }
+          return ((rs[0] + rs[1]) + (rs[2] + rs[3])) + ((rs[4] + rs[5]) + (rs[6] + rs[7]));
+        };
+        // Raises the maximum to m_new; returns what the sum and O so far scale with.
+        auto raise = [&](float m_new) {
+          float alpha = 1.f;
+          if (m_new > m + 8.0f) {
+            alpha = ptx::ex2(m - m_new);
+            m = m_new;
           }
+          lsum *= alpha;
+          if (t > walk.t0) chunk_scale_columns<D>(tO, alpha);  // the first P V overwrites O
+          return alpha;
+        };
+
+        bool have_b = false;
+        auto wait_b = [&]() {
+          if (!have_b) ok = __all_sync(~0u, wait(S::SB(i), s_phase));
+          have_b = true;
+        };
+        ok = __all_sync(~0u, wait(S::SA(i), s_phase));
+        if (!ok) break;
+        load(0, tA);
+        float rs = 0.f;
+        if (used) {
+          const float mx = row_max();
+          if (__any_sync(~0u, mx > m + 8.0f)) {
+            // half b is issued behind the last P V: with it O stands still
+            wait_b();
+            if (!ok) break;
+            ptx::tc_fence_after();
+            raise(fmaxf(m, mx));
+          }
+          rs = exponentials(tA);
+        }
+        wait_b();
+        if (!ok) break;
+        load(1, tB);
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_leader(read);
+        if (used) {
+          const float mx = row_max();
+          if (__any_sync(~0u, mx > m + 8.0f)) {
+            // half a's P is scaled too (its second rounding to fp16, in the few tiles where
+            // a maximum grows that much)
+            ptx::tmem_wait_st();
+            const float alpha = raise(fmaxf(m, mx));
+            rs *= alpha;
+            chunk_scale_p(tA, alpha);
+          }
+          lsum += rs + exponentials(tA + 32);
           ptx::tmem_wait_st();
         }
+        s_phase ^= 1u;
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive_leader(p_full);

@@ -161,10 +161,11 @@ __global__ void __launch_bounds__(448, 1)
                           static_cast<size_t>(walk.item) * 128;
       constexpr int P = D / 32;
       ConvertRegs<P> x;
-      convert_load<D, P>(x, c.k_codes, c.k_scales, row0, 0, tid);
+      auto key = [](int r) { return r; };
+      convert_load<D, P>(x, c.k_codes, c.k_scales, row0, 0, tid, key);
       if (!__all_sync(~0u, wait(S::KEMPTY(kb), ((unit >> 1) & 1) ^ 1u))) break;
       convert_store<P>(x, sbase + S::kOffK + kb * S::kTile, tid,
-                       rows_held(c, walk.b) - walk.item * 128, tile_offset);
+                       rows_held(c, walk.b) - walk.item * 128, key, tile_offset);
       ptx::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bar(S::KFULL(kb)));
