@@ -177,6 +177,89 @@ __device__ __forceinline__ int tiles_before(const Kv4AttendParams& p, int upto, 
   return __reduce_add_sync(~0u, sum) * p.c.H * p.row_blocks;
 }
 
+// A lane's quarter of a query row as the fragments of S^T = K Q^T: lane (g, tig) of
+// step k holds values 4 k .. 4 k + 3 of its D / 4 consecutive ones of row g. Scaled to
+// fp16 by a power of two per row; returns what the row's scores are multiplied with.
+template <int D, int kDtype>
+__device__ __forceinline__ float query_fragments(const uint4 (&w)[D / 32], float scale_log2,
+                                                 uint32_t (&frag)[D / 16][2]) {
+  float2 v[D / 8];
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    v[4 * i] = unpack2<kDtype>(w[i].x);
+    v[4 * i + 1] = unpack2<kDtype>(w[i].y);
+    v[4 * i + 2] = unpack2<kDtype>(w[i].z);
+    v[4 * i + 3] = unpack2<kDtype>(w[i].w);
+  }
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) amax = fmaxf(amax, fmaxf(fabsf(v[i].x), fabsf(v[i].y)));
+  amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 1));
+  amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 2));
+  const float f = row_factor(amax);
+#pragma unroll
+  for (int k = 0; k < D / 16; ++k) {
+    frag[k][0] = pack2<SA_DTYPE_FP16>(v[2 * k].x * f, v[2 * k].y * f);
+    frag[k][1] = pack2<SA_DTYPE_FP16>(v[2 * k + 1].x * f, v[2 * k + 1].y * f);
+  }
+  return score_factor(scale_log2, f);
+}
+
+// This lane's quarter of query row `row` of (sequence b, KV head h); zeros if not there.
+template <int D>
+__device__ __forceinline__ void load_query(const Kv4AttendParams& p, int b, int h, int row,
+                                           bool there, int tig, uint4 (&w)[D / 32]) {
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) w[i] = make_uint4(0u, 0u, 0u, 0u);
+  if (!there) return;
+  const uint16_t* q = static_cast<const uint16_t*>(p.q.data) + b * p.q.sb +
+                      (row / p.group) * p.q.st + (h * p.group + row % p.group) * p.q.sh +
+                      tig * (D / 4);
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(q) + i);
+}
+
+// A warp tile's K codes as operand registers: [word][16-row half][rows g, g + 8][pair].
+// `kc`, `ksc`: the tile's codes and scales in shared memory.
+template <int D>
+struct KeyWords {
+  uint32_t w[2][2][D / 32], s[2][2];
+  __device__ __forceinline__ void load(uint32_t kc, uint32_t ksc, int g, int tig) {
+#pragma unroll
+    for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+      for (int hi = 0; hi < 2; ++hi) {
+        const int row = sub * 16 + tile_row<D>(g + 8 * hi);
+        if constexpr (D == 128) {
+          const uint4 x = lds128(kc + row * 64 + tig * 16);
+          w[sub][hi][0] = x.x;
+          w[sub][hi][1] = x.y;
+          w[sub][hi][D / 32 - 2] = x.z;
+          w[sub][hi][D / 32 - 1] = x.w;
+          s[sub][hi] = lds16(ksc + row * 8 + tig * 2);
+        } else {
+          const uint2 x = lds64(kc + row * 32 + tig * 8);
+          w[sub][hi][0] = x.x;
+          w[sub][hi][D / 32 - 1] = x.y;
+          s[sub][hi] = lds8(ksc + row * 4 + tig);
+        }
+      }
+  }
+  // Word `i` (two steps of 16 values): a[half][rows g, g + 8][pair], scaled.
+  __device__ __forceinline__ void convert(int i, uint32_t (&a)[2][2][4]) const {
+#pragma unroll
+    for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+      for (int hi = 0; hi < 2; ++hi) {
+        codes_to_f16(w[sub][hi][i], a[sub][hi]);
+        const uint32_t sc =
+            scale_f16x2(D == 128 ? (s[sub][hi] >> (8 * (i >> 1))) & 255u : s[sub][hi]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) a[sub][hi][k] = mul_f16x2(a[sub][hi][k], sc);
+      }
+  }
+};
+
 template <int D, int NT, int kDtype, bool kScores>
 __global__ void __launch_bounds__(128, DecodeShape<D, NT>::kBlocksPerSm)
     kv4_decode_kernel(const __grid_constant__ Kv4AttendParams p) {
@@ -251,57 +334,25 @@ __global__ void __launch_bounds__(128, DecodeShape<D, NT>::kBlocksPerSm)
     const int my_nt = NT == 1 ? 0 : warp, q_row = row0 + my_nt * 8 + g;
     const bool has_row = my_nt < NT && q_row < n_rows;
     uint4 qw[D / 32];
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) qw[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (has_row) {
-      const uint16_t* q = static_cast<const uint16_t*>(p.q.data) + b * p.q.sb +
-                          (q_row / p.group) * p.q.st +
-                          (h * p.group + q_row % p.group) * p.q.sh + tig * (D / 4);
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) qw[i] = __ldg(reinterpret_cast<const uint4*>(q) + i);
-    }
+    load_query<D>(p, b, h, q_row, has_row, tig, qw);
     int next = t0 + warp;  // next tile to load; the ring is empty here
     for (int s = 0; s < S::kStages && ok && next < t1; ++s, next += S::kWarps, ++pending)
       fill(next, st + s < S::kStages ? st + s : st + s - S::kStages);
 
-    // Query fragments: lane (g, tig) of step k holds values 4 k .. 4 k + 3 of its
-    // D / 4 consecutive ones of query row g. Scaled to fp16 by a power of two a row.
-    uint32_t qf[NT == 1 ? KS : 1][2];
-    float sl[NT][2];  // scale * log2 e / row factor of this lane's query columns
+    uint32_t qf[KS][2];  // the lane's own row; with NT > 1 all rows are in shared memory
+    float sl[NT][2];     // scale * log2 e / row factor of this lane's query columns
     float* s_sl = reinterpret_cast<float*>(smem + S::kOffSl);
     if constexpr (NT > 1) __syncthreads();  // the previous unit is done with them
     if (my_nt < NT) {
-      float2 v[D / 8];
-      float amax = 0.f;
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        v[4 * i] = unpack2<kDtype>(qw[i].x);
-        v[4 * i + 1] = unpack2<kDtype>(qw[i].y);
-        v[4 * i + 2] = unpack2<kDtype>(qw[i].z);
-        v[4 * i + 3] = unpack2<kDtype>(qw[i].w);
-      }
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) amax = fmaxf(amax, fmaxf(fabsf(v[i].x), fabsf(v[i].y)));
-      amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 1));
-      amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 2));
-      const float f = row_factor(amax);
-#pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        const uint32_t x = pack2<SA_DTYPE_FP16>(v[2 * k].x * f, v[2 * k].y * f);
-        const uint32_t y = pack2<SA_DTYPE_FP16>(v[2 * k + 1].x * f, v[2 * k + 1].y * f);
-        if constexpr (NT == 1) {
-          qf[k][0] = x;
-          qf[k][1] = y;
-        } else {
-          *reinterpret_cast<uint2*>(smem + S::kOffQ + ((k * NT + my_nt) * 32 + lane) * 8) =
-              make_uint2(x, y);
-        }
-      }
-      const float scale = score_factor(p.scale_log2, f);
+      const float scale = query_fragments<D, kDtype>(qw, p.scale_log2, qf);
       if constexpr (NT == 1) {  // lane 4 n (or any of its four) holds row n's
         sl[0][0] = __shfl_sync(~0u, scale, 8 * tig);
         sl[0][1] = __shfl_sync(~0u, scale, 8 * tig + 4);
       } else {
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+          *reinterpret_cast<uint2*>(smem + S::kOffQ + ((k * NT + my_nt) * 32 + lane) * 8) =
+              make_uint2(qf[k][0], qf[k][1]);
         if (tig == 0) s_sl[my_nt * 8 + g] = scale;
       }
     }
@@ -338,26 +389,8 @@ __global__ void __launch_bounds__(128, DecodeShape<D, NT>::kBlocksPerSm)
 
       // ---- S^T
       float s[2][NT][4];
-      uint32_t kw[2][2][KW], ksb[2][2];
-#pragma unroll
-      for (int sub = 0; sub < 2; ++sub)
-#pragma unroll
-        for (int hi = 0; hi < 2; ++hi) {
-          const int row = sub * 16 + tile_row<D>(g + 8 * hi);
-          if constexpr (D == 128) {
-            const uint4 w = lds128(kc + row * 64 + tig * 16);
-            kw[sub][hi][0] = w.x;
-            kw[sub][hi][1] = w.y;
-            kw[sub][hi][KW - 2] = w.z;
-            kw[sub][hi][KW - 1] = w.w;
-            ksb[sub][hi] = lds16(ksc + row * 8 + tig * 2);
-          } else {
-            const uint2 w = lds64(kc + row * 32 + tig * 8);
-            kw[sub][hi][0] = w.x;
-            kw[sub][hi][KW - 1] = w.y;
-            ksb[sub][hi] = lds8(ksc + row * 4 + tig);
-          }
-        }
+      KeyWords<D> kw;
+      kw.load(kc, ksc, g, tig);
 #pragma unroll
       for (int sub = 0; sub < 2; ++sub)
 #pragma unroll
@@ -367,16 +400,7 @@ __global__ void __launch_bounds__(128, DecodeShape<D, NT>::kBlocksPerSm)
 #pragma unroll
       for (int w = 0; w < KW; ++w) {  // a word is two steps
         uint32_t a[2][2][4];
-#pragma unroll
-        for (int sub = 0; sub < 2; ++sub)
-#pragma unroll
-          for (int hi = 0; hi < 2; ++hi) {
-            codes_to_f16(kw[sub][hi][w], a[sub][hi]);
-            const uint32_t sc = scale_f16x2(D == 128 ? (ksb[sub][hi] >> (8 * (w >> 1))) & 255u
-                                                     : ksb[sub][hi]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) a[sub][hi][i] = mul_f16x2(a[sub][hi][i], sc);
-          }
+        kw.convert(w, a);
 #pragma unroll
         for (int half = 0; half < 2; ++half)
 #pragma unroll
@@ -598,10 +622,11 @@ __global__ void __launch_bounds__(128, DecodeShape<D, NT>::kBlocksPerSm)
   }
 }
 
-// Merge of the partial results of kv4_decode_kernel, W warps per query row, and the rows'
-// weights. Blocks below join_blocks merge; the others add weights, kJoinKeys cache
-// rows of one (sequence, KV head) each: they derive the log-sum-exp of its query rows
-// from the same partial results, so no order among blocks is needed.
+// Merge of the partial results of kv4_decode_kernel, W warps per query row, and, where
+// that left the scores (up to 8 query rows), the rows' weights. Blocks below
+// join_blocks merge; the others add weights, kJoinKeys cache rows of one (sequence, KV
+// head) each: they derive the log-sum-exp of its query rows from the same partial
+// results, so no order among blocks is needed.
 constexpr int kJoinKeys = 512;
 
 template <int D, int kRows, int W, int kDtype>
@@ -610,7 +635,8 @@ __global__ void __launch_bounds__(128)
   const Kv4& c = p.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool joins = static_cast<int>(blockIdx.x) < join_blocks;
-  // join: block = (unit, 4 / W rows of it); weights: block = (head plane, chunk of rows)
+  // join: block = (unit, 4 / W rows of it); weights (8 query rows or fewer): block =
+  // (head plane, chunk of cache rows)
   constexpr int kGroups = kRows * W / 4;
   const int chunks = (c.N + kJoinKeys - 1) / kJoinKeys;
   const int id = joins ? blockIdx.x / kGroups : (blockIdx.x - join_blocks) / chunks;
@@ -726,9 +752,14 @@ __global__ void __launch_bounds__(128)
                                                   pack2<kDtype>(acc[V - 2] * inv, acc[V - 1] * inv));
     else
       *reinterpret_cast<uint32_t*>(dst) = pack2<kDtype>(acc[0] * inv, acc[1] * inv);
-    if (lane == 0 && p.lse != nullptr)
-      p.lse[(static_cast<size_t>(b) * p.heads + hq) * p.T + t] =
-          sum == 0.f ? -INFINITY : (mx + log2f(sum)) * 0.69314718055994531f;
+    if (lane == 0) {
+      const float lse2 = sum == 0.f ? -INFINITY : mx + log2f(sum);
+      if (p.lse != nullptr)
+        p.lse[(static_cast<size_t>(b) * p.heads + hq) * p.T + t] = lse2 * 0.69314718055994531f;
+      if (kRows > 8 && p.add_weight)
+        p.row_nlse[(static_cast<size_t>(b) * c.H + h) * p.score_rows + row] =
+            sum == 0.f ? -INFINITY : -lse2;
+    }
     return;
   }
 
@@ -768,6 +799,181 @@ __global__ void __launch_bounds__(128)
       sum += ptx::ex2(x.x - s_lse[r]) + ptx::ex2(x.y - s_lse[r + 1]);
     }
     c.weight[plane + j] += sum;
+  }
+}
+
+// Weights drawn by 9 to 64 query rows: one more pass over K, its scores now against
+// known log-sum-exps. Reads D / 2 + D / 16 bytes a cache row, where leaving the scores
+// for the join moves 8 bytes a cache row per query row (32 rows, 8 x 8 x 32768: 306 us
+// in all against 200). A warp owns its cache rows, so there are no atomics.
+template <int D>
+struct DecodeWeightShape {
+  static constexpr int kTile = 32, kWarps = 4, kStages = 4, kNt = 8;
+  static constexpr int kCodes = kTile * D / 2, kScales = kTile * D / 16;
+  static constexpr int kStageBytes = kCodes + kScales;
+  static constexpr int kOffQ = kWarps * kStages * kStageBytes;  // fragments of 64 rows
+  static constexpr int kOffSl = kOffQ + 64 * D * 2;             // score factor, -lse
+  static constexpr int kOffBar = kOffSl + 64 * 8;
+  static constexpr int kSmem = kOffBar + kWarps * kStages * 8 + 16;
+  static constexpr int kBlocksPerSm = 4;
+};
+
+template <int D, int kDtype>
+__global__ void __launch_bounds__(128, 4)
+    kv4_decode_weight_kernel(const __grid_constant__ Kv4AttendParams p) {
+  using S = DecodeWeightShape<D>;
+  constexpr int KS = D / 16, KW = D / 32;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const Kv4& c = p.c;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, tig = lane & 3;
+  const uint32_t sbase = ptx::smem_addr(smem);
+  const uint32_t ring = sbase + warp * S::kStages * S::kStageBytes;
+  const uint32_t bars = sbase + S::kOffBar + warp * S::kStages * 8;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kSmem - 16);
+  float2* s_row = reinterpret_cast<float2*>(smem + S::kOffSl);
+  if (threadIdx.x == 0) *abort_flag = 0;
+  if (lane == 0) {
+    for (int s = 0; s < S::kStages; ++s) ptx::mbar_init(bars + 8 * s, 1);
+    ptx::fence_mbar_init();
+  }
+  __syncthreads();
+  const Line line = line_of(p, gridDim.x, S::kTile, lane);
+  int at = min(static_cast<long long>(blockIdx.x) * line.share,
+               static_cast<long long>(line.total));
+  const int stop = min(at + line.share, line.total);
+  int b = 0, b0 = 0, per_unit = 1;
+  if (at < stop) find_sequence(p, at, S::kTile, lane, b, b0, per_unit);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the join's log-sum-exps
+  int st = 0, pending = 0;
+  uint32_t phase = 0;
+  bool ok = true;
+
+  while (at < stop) {
+    if (at >= b0 + per_unit * c.H) find_sequence(p, at, S::kTile, lane, b, b0, per_unit);
+    const int h = (at - b0) / per_unit;
+    const int t0 = at - b0 - h * per_unit;
+    const int t1 = min(per_unit, t0 + (stop - at));
+    const int held = rows_held(c, b), n_tok = tokens_of(p.counts, b, p.T);
+    const int n_rows = n_tok * p.group, n_nt = (n_rows + 7) / 8;
+    const size_t plane = (static_cast<size_t>(b) * c.H + h) * c.N;
+    auto fill = [&](int tile, int stage) {
+      const uint32_t bar = bars + 8 * stage;
+      if (lane == 0) ptx::mbar_arrive_expect_tx(bar, S::kStageBytes);
+      __syncwarp();
+      const size_t row = plane + static_cast<size_t>(tile) * S::kTile;
+      if (lane < 2)
+        bulk_load(ring + stage * S::kStageBytes + (lane == 0 ? 0 : S::kCodes),
+                  lane == 0 ? c.k_codes + row * (D / 2) : c.k_scales + row * (D / 16),
+                  lane == 0 ? S::kCodes : S::kScales, bar);
+    };
+    int next = t0 + warp;
+    for (int s = 0; s < S::kStages && ok && next < t1; ++s, next += S::kWarps, ++pending)
+      fill(next, st + s < S::kStages ? st + s : st + s - S::kStages);
+    __syncthreads();  // the previous unit is done with the queries
+    for (int nt = warp; nt < n_nt; nt += S::kWarps) {
+      const int row = nt * 8 + g;
+      uint4 qw[D / 32];
+      uint32_t qf[KS][2];
+      load_query<D>(p, b, h, row, row < n_rows, tig, qw);
+      const float scale = query_fragments<D, kDtype>(qw, p.scale_log2, qf);
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+        *reinterpret_cast<uint2*>(smem + S::kOffQ + ((nt * KS + k) * 32 + lane) * 8) =
+            make_uint2(qf[k][0], qf[k][1]);
+      if (tig == 0)  // rows that are not there draw nothing
+        s_row[row] = make_float2(
+            scale, row < n_rows
+                       ? p.row_nlse[(static_cast<size_t>(b) * c.H + h) * p.score_rows + row]
+                       : -INFINITY);
+    }
+    __syncthreads();
+    const int open = p.causal ? max(held - n_tok + 1, 0) : held;
+
+    for (int t = t0 + warp; ok && t < t1; t += S::kWarps) {
+      const int j0 = t * S::kTile;
+      // the weights so far, asked for ahead: lane (g, 0) owns rows g, g + 8 of each half
+      float w[2][2];
+#pragma unroll
+      for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+        for (int hi = 0; hi < 2; ++hi) {
+          const int j = j0 + sub * 16 + tile_row<D>(g + 8 * hi);
+          w[sub][hi] = tig == 0 && j < held ? c.weight[plane + j] : 0.f;
+        }
+      ok = __all_sync(~0u, ptx::mbar_wait(bars + 8 * st, phase, abort_flag, c.status));
+      if (!ok) break;
+      --pending;
+      const uint32_t kc = ring + st * S::kStageBytes;
+      KeyWords<D> kw;
+      kw.load(kc, kc + S::kCodes, g, tig);
+      uint32_t a[KW][2][2][4];
+#pragma unroll
+      for (int i = 0; i < KW; ++i) kw.convert(i, a[i]);
+      __syncwarp();  // every lane has read the stage
+      if (next < t1) {
+        fill(next, st);
+        next += S::kWarps;
+        ++pending;
+      }
+      if (++st == S::kStages) {
+        st = 0;
+        phase ^= 1u;
+      }
+      const bool edge = j0 + S::kTile > open;
+      float sum[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll 1
+      for (int nt = 0; nt < n_nt; ++nt) {
+        float s[2][4];
+#pragma unroll
+        for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[sub][i] = 0.f;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const uint2 f = lds64(sbase + S::kOffQ + ((nt * KS + k) * 32 + lane) * 8);
+          const int i = k >> 1, half = k & 1;
+#pragma unroll
+          for (int sub = 0; sub < 2; ++sub)
+            mma_16816(s[sub], a[i][sub][0][2 * half], a[i][sub][1][2 * half],
+                      a[i][sub][0][2 * half + 1], a[i][sub][1][2 * half + 1], f.x, f.y);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = nt * 8 + 2 * tig + i;
+          const float2 row = s_row[r];
+          const int end = edge ? rows_seen(p, held, n_tok, r / p.group) : held;
+#pragma unroll
+          for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+            for (int hi = 0; hi < 2; ++hi) {
+              const float e = ptx::ex2(fmaf(s[sub][2 * hi + i], row.x, row.y));
+              const int j = j0 + sub * 16 + tile_row<D>(g + 8 * hi);
+              sum[sub][hi] += edge && j >= end ? 0.f : e;
+            }
+        }
+      }
+#pragma unroll
+      for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+        for (int hi = 0; hi < 2; ++hi) {
+          float x = sum[sub][hi];
+          x += __shfl_xor_sync(~0u, x, 1);
+          x += __shfl_xor_sync(~0u, x, 2);
+          const int j = j0 + sub * 16 + tile_row<D>(g + 8 * hi);
+          if (tig == 0 && j < held) c.weight[plane + j] = w[sub][hi] + x;
+        }
+    }
+    at += t1 - t0;
+  }
+  // after an abort: copies still under way land before the block's memory goes
+  volatile int none = 0;
+  for (; pending > 0; --pending) {
+    ptx::mbar_wait(bars + 8 * st, phase, &none, c.status);
+    if (++st == S::kStages) {
+      st = 0;
+      phase ^= 1u;
+    }
   }
 }
 

@@ -253,8 +253,11 @@ AttendPlan plan_attend(const sa_kv4_cache* c, int heads, int T, bool weights) {
     a.off_ml = off;
     off += align_up(slots * 8 * a.nt * sizeof(float2), 256);
     a.score_rows = (rows + 1) / 2 * 2;
+    // for the weights: every score, or with more than 8 query rows their log-sum-exps
     a.off_scores = off;
-    if (weights) off += align_up(planes * c->capacity * a.score_rows * sizeof(float), 256);
+    if (weights)
+      off += align_up((a.nt == 1 ? planes * c->capacity : planes) * a.score_rows * sizeof(float),
+                      256);
   } else {
     auto take = [&](size_t bytes) {
       const size_t at = off;
@@ -294,24 +297,30 @@ bool launch_decode(const sa::Kv4AttendParams& p, cudaStream_t s) {
   auto join = [&](auto kernel, int warps) {
     const int merge = units * (S::kRows * warps / 4);
     launch_after(kernel, dim3(merge + (kScores ? p.c.B * p.c.H * chunks : 0)), dim3(128),
-                 p.score_rows * sizeof(float), s, p, blocks, merge);
+                 kScores ? p.score_rows * sizeof(float) : 0, s, p, blocks, merge);
   };
   if (blocks > 8 * units)
     join(sa::kv4_join_kernel<D, S::kRows, 4, kDtype>, 4);
   else
     join(sa::kv4_join_kernel<D, S::kRows, 1, kDtype>, 1);
+  if (p.add_weight && !kScores) {
+    using W = sa::DecodeWeightShape<D>;
+    if (!allow_smem<sa::kv4_decode_weight_kernel<D, kDtype>>(W::kSmem)) return false;
+    sa::Kv4AttendParams q = p;
+    q.row_blocks = 1;  // a unit has all query rows
+    launch_after(sa::kv4_decode_weight_kernel<D, kDtype>,
+                 dim3(std::min(sm_count(), kMostSms) * W::kBlocksPerSm), dim3(128), W::kSmem, s, q);
+  }
   return true;
 }
 
 template <int D, int kDtype>
 bool launch_decode_nt(const sa::Kv4AttendParams& p, int nt, cudaStream_t s) {
-  if (p.add_weight)
-    return nt == 1   ? launch_decode<D, 1, kDtype, true>(p, s)
-           : nt == 2 ? launch_decode<D, 2, kDtype, true>(p, s)
-                     : launch_decode<D, 4, kDtype, true>(p, s);
-  return nt == 1   ? launch_decode<D, 1, kDtype, false>(p, s)
-         : nt == 2 ? launch_decode<D, 2, kDtype, false>(p, s)
-                   : launch_decode<D, 4, kDtype, false>(p, s);
+  if (nt == 1)
+    return p.add_weight ? launch_decode<D, 1, kDtype, true>(p, s)
+                        : launch_decode<D, 1, kDtype, false>(p, s);
+  return nt == 2 ? launch_decode<D, 2, kDtype, false>(p, s)
+                 : launch_decode<D, 4, kDtype, false>(p, s);
 }
 
 template <int D, int kDtype>
@@ -485,6 +494,7 @@ SA_API int sa_kv4_attend(const sa_kv4_cache* c, const sa_rows* Q, const sa_rows*
   p.part_o = reinterpret_cast<float*>(ws + plan.off_o);
   p.part_ml = reinterpret_cast<float2*>(ws + plan.off_ml);
   p.scores = reinterpret_cast<float*>(ws + plan.off_scores);
+  p.row_nlse = p.scores;
   p.score_rows = plan.score_rows;
   DeviceGuard guard(device);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
