@@ -214,7 +214,8 @@ __global__ void __launch_bounds__(256)
     kv4_stage_kernel(const __grid_constant__ Kv4AttendParams p) {
   constexpr int C = D / 8;  // 16-byte pieces of a row
   const Kv4& c = p.c;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  begin_early();
+  wait_for_previous();
   if (static_cast<int>(blockIdx.x) >= p.q_tiles) {
     if (blockIdx.y != 0 || blockIdx.z != 0) return;
     if (static_cast<int>(blockIdx.x) == p.q_tiles) {
@@ -443,7 +444,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(512, 1)
   cluster_sync();  // both blocks' barriers are there
   ptx::tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // staged queries and schedule
+  wait_for_previous();  // staged queries and schedule
 
   LineWalk walk = line_range(p.line, c.B, pair, pairs);
   auto wait = [&](int which, uint32_t parity) {
@@ -814,7 +815,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(512, 1)
 template <int D, int kDtype>
 __global__ void __launch_bounds__(128)
     kv4_chunk_join_kernel(const __grid_constant__ Kv4AttendParams p, int blocks) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  begin_early();
+  wait_for_previous();
   const Kv4& c = p.c;
   SplitItem split;
   if (!split.find(p.line, c.B, blocks, blockIdx.x)) return;

@@ -281,7 +281,8 @@ __global__ void __launch_bounds__(128, DecodeShape<D, NT>::kBlocksPerSm)
     ptx::fence_mbar_init();
   }
   __syncthreads();
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  begin_early();
+  wait_for_previous();
 
   const Line line = line_of(p, gridDim.x, S::kTile, lane);
   int at = min(static_cast<long long>(blockIdx.x) * line.share,
@@ -648,7 +649,8 @@ __global__ void __launch_bounds__(128)
   const Line line = line_of(p, blocks, 32, lane);
   const int b0 = tiles_before(p, b, 32, lane);
   const int per_unit = unit_tiles(p, b, 32);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  begin_early();
+  wait_for_previous();
   if (n_rows == 0) return;
 
   // Partial results of one query row: `n` slots from `first` on.
@@ -844,7 +846,8 @@ __global__ void __launch_bounds__(128, 4)
   const int stop = min(at + line.share, line.total);
   int b = 0, b0 = 0, per_unit = 1;
   if (at < stop) find_sequence(p, at, S::kTile, lane, b, b0, per_unit);
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the join's log-sum-exps
+  begin_early();
+  wait_for_previous();  // the join's log-sum-exps
   int st = 0, pending = 0;
   uint32_t phase = 0;
   bool ok = true;

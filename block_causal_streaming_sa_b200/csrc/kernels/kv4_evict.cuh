@@ -65,6 +65,8 @@ __global__ void __launch_bounds__(1024, 1)
   const int blocks = static_cast<int>(cluster.num_blocks());
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const unsigned below_lane = (1u << lane) - 1;
+  begin_early();
+  wait_for_previous();
   const int n = rows_held(c, b);
   const size_t plane = (static_cast<size_t>(b) * c.H + h) * c.N;
 

@@ -13,11 +13,22 @@
 #include <cuda_fp16.h>
 
 #include "../sa_internal.h"
+#include "ptx.cuh"
 
 namespace sa {
 
 constexpr unsigned kMaxScaleByte = 226;   // 10240 = 1.25 * 2^13
 constexpr float kMaxStored = 61440.0f;    // 6 * 10240
+
+// Launches may begin while the kernel before them on the stream drains (the host asks
+// for that): every kernel lets the next one begin early and waits, in every block,
+// until the kernel before it has finished and its writes can be seen.
+__device__ __forceinline__ void begin_early() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
 
 // One cache as the kernels see it (include/sa.h: sa_kv4_cache).
 struct Kv4 {
@@ -64,26 +75,27 @@ __device__ __forceinline__ float scale_value(unsigned byte) {
   return __half2float(__ushort_as_half(static_cast<unsigned short>(byte << 7)));
 }
 
-// x * inv (inv = 1 / scale) moved to the nearest multiple of 2^-16: a quotient
+// x * inv of a pair (inv = 1 / scale) moved to the nearest multiple of 2^-16: a quotient
 // that equals a midpoint between two codes comes out as that midpoint whatever
 // inv's rounding did (error < 2^-20), and no other quotient can reach it (x and
 // midpoint * scale have at most 11 significant bits, so they differ by 2^-13 of
 // the code range or more). Ties then go to the even code as in exact arithmetic.
-__device__ __forceinline__ float snap(float x, float inv) {
-  return __fsub_rn(__fmaf_rn(x, inv, 192.0f), 192.0f);
+__device__ __forceinline__ void snap2(float2& x, float inv) {
+  ptx::ffma2(x.x, x.y, x.x, x.y, inv, inv, 192.0f, 192.0f);
+  ptx::fadd2(x.x, x.y, x.x, x.y, -192.0f, -192.0f);
 }
 
 // Eight codes (e2m1, nearest even, saturating) of eight values into one word.
-__device__ __forceinline__ uint32_t e2m1x8(const float (&q)[8]) {
+__device__ __forceinline__ uint32_t e2m1x8(float2 a, float2 b, float2 c, float2 d) {
   uint32_t w;
-  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
-      "mov.b32 %0, {a, b, c, d};\n\t}"
+  asm("{\n\t.reg .b8 p, q, r, s;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 p, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 q, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 r, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 s, %8, %7;\n\t"
+      "mov.b32 %0, {p, q, r, s};\n\t}"
       : "=r"(w)
-      : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y), "f"(d.x), "f"(d.y));
   return w;
 }
 

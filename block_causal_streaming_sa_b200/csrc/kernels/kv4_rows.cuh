@@ -1,7 +1,8 @@
 // Appending rows to a 4-bit cache (quantisation) and reading them back.
 //
 // Both are bound by HBM: append reads 4 D bytes a row and head and writes
-// D + D / 8 + 8, read the reverse. A thread owns one block of 16 values of K and
+// D + D / 8 + 8, read the reverse (10800 rows x 12 heads, D 128, 85 MB: 24 and 18 us; a
+// plain copy that moves as much takes 25). A thread owns one block of 16 values of K and
 // the same block of V: two 16-byte loads each, one 8-byte and one 1-byte store.
 // The threads of a warp cover consecutive blocks of consecutive tokens of one
 // head, so loads are whole lines of the input rows and the stores of a head's
@@ -19,40 +20,53 @@ struct Kv4AppendParams {
   int T, replace;
 };
 
+// Largest magnitude of both halves of two words; NaN if any is.
+template <int kDtype>
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if constexpr (kDtype == SA_DTYPE_FP16)
+    asm("{\n\t.reg .b32 x, y;\n\tabs.f16x2 x, %1;\n\tabs.f16x2 y, %2;\n\t"
+        "max.NaN.f16x2 %0, x, y;\n\t}"
+        : "=r"(r)
+        : "r"(a), "r"(b));
+  else
+    asm("{\n\t.reg .b32 x, y;\n\tabs.bf16x2 x, %1;\n\tabs.bf16x2 y, %2;\n\t"
+        "max.NaN.bf16x2 %0, x, y;\n\t}"
+        : "=r"(r)
+        : "r"(a), "r"(b));
+  return r;
+}
+
 template <int kDtype>
 __device__ __forceinline__ void quantise_block(const uint4 (&in)[2], uint2* codes, uint8_t* scale,
                                                bool& bad) {
-  float x[16];
   const uint32_t w[8] = {in[0].x, in[0].y, in[0].z, in[0].w, in[1].x, in[1].y, in[1].z, in[1].w};
-  float amax = 0.f;
-  bool odd = false;  // some value is not finite or beyond the largest stored one
+  // the maximum on packed pairs, two words an instruction
+  uint32_t m = max_abs2<kDtype>(w[0], w[1]);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float2 p = unpack2<kDtype>(w[i]);
-    x[2 * i] = p.x;
-    x[2 * i + 1] = p.y;
-    amax = fmaxf(amax, fmaxf(fabsf(p.x), fabsf(p.y)));
-    odd |= !(fabsf(p.x) <= kMaxStored) | !(fabsf(p.y) <= kMaxStored);
-  }
-  if (odd) {
+  for (int i = 2; i < 8; i += 2)
+    m = max_abs2<kDtype>(m, max_abs2<kDtype>(w[i], w[i + 1]));
+  const float2 m2 = unpack2<kDtype>(max_abs2<kDtype>(m, (m >> 16) | (m << 16)));
+  float amax = m2.x;
+  float2 x[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = unpack2<kDtype>(w[i]);
+  if (!(amax <= kMaxStored)) {  // some value is not finite or beyond the largest stored one
     bad = true;
     amax = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < 8; ++i) {
       // clamps infinities; fminf / fmaxf turn a NaN into the bound
-      x[i] = fmaxf(fminf(x[i], kMaxStored), -kMaxStored);
-      amax = fmaxf(amax, fabsf(x[i]));
+      x[i].x = fmaxf(fminf(x[i].x, kMaxStored), -kMaxStored);
+      x[i].y = fmaxf(fminf(x[i].y, kMaxStored), -kMaxStored);
+      amax = fmaxf(amax, fmaxf(fabsf(x[i].x), fabsf(x[i].y)));
     }
   }
   const unsigned byte = scale_byte(amax);
   const float inv = byte != 0 ? __fdiv_rn(1.0f, scale_value(byte)) : 0.f;
-  float q[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = snap(x[i], inv);
-  const uint32_t lo = e2m1x8(q);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = snap(x[8 + i], inv);
-  *codes = make_uint2(lo, e2m1x8(q));
+  for (int i = 0; i < 8; ++i) snap2(x[i], inv);
+  *codes = make_uint2(e2m1x8(x[0], x[1], x[2], x[3]), e2m1x8(x[4], x[5], x[6], x[7]));
   *scale = static_cast<uint8_t>(byte);
 }
 
@@ -63,6 +77,8 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const __grid_constant__
   constexpr int NB = D / 16;
   const Kv4& c = p.c;
   const int b = blockIdx.z, h = blockIdx.y;
+  begin_early();
+  wait_for_previous();
   const int held = rows_held(c, b);
   const int last = p.replace ? min(max(c.seq[kSeqLast * c.B + b], 0), held) : 0;
   const int base = held - last;
@@ -148,6 +164,8 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(const __grid_constant__ K
   constexpr int NB = D / 16;
   const Kv4& c = p.c;
   const int b = blockIdx.z, h = blockIdx.y;
+  begin_early();
+  wait_for_previous();
   const int held = rows_held(c, b);
   int base = p.first, n = p.T;
   if (p.first < 0) {

@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(448, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the attention's log-sum-exps
+  wait_for_previous();  // the attention's log-sum-exps
 
   LineWalk walk = line_range(p.weight_line, c.B, blockIdx.x, gridDim.x);
   auto wait = [&](int which, uint32_t parity) {
@@ -269,7 +269,8 @@ __global__ void __launch_bounds__(448, 1)
 // Weights of key tiles that lie in several blocks' ranges, summed in their order.
 __global__ void __launch_bounds__(128)
     kv4_weight_join_kernel(const __grid_constant__ Kv4AttendParams p, int blocks) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  begin_early();
+  wait_for_previous();
   const Kv4& c = p.c;
   SplitItem split;
   if (!split.find(p.weight_line, c.B, blocks, blockIdx.x)) return;

@@ -145,6 +145,24 @@ int check_workspace(const void* ws, size_t bytes, size_t need, int device) {
   return SA_OK;
 }
 
+// Launch that may begin while the kernel before it on the stream drains; the kernel
+// itself waits until that one has finished (wait_for_previous, in every block).
+template <typename... P, typename... A>
+void launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                  A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 int launched(const char* what) {
   const cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess) return SA_OK;
@@ -197,24 +215,6 @@ bool allow_smem(int bytes, int regs = 0) {
     return false;
   done[dev].store(true, std::memory_order_relaxed);
   return true;
-}
-
-// Launch that may begin while the kernel before it on the stream drains; the kernel
-// itself waits (griddepcontrol.wait) before it reads what that one wrote.
-template <typename... P, typename... A>
-void launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
-                  A... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 // How an attention is run: sizes that follow from the shape alone, so that the
@@ -289,7 +289,8 @@ bool launch_decode(const sa::Kv4AttendParams& p, cudaStream_t s) {
   using S = sa::DecodeShape<D, NT>;
   if (!allow_smem<sa::kv4_decode_kernel<D, NT, kDtype, kScores>>(S::kSmem)) return false;
   const int blocks = std::min(sm_count(), kMostSms) * S::kBlocksPerSm;
-  sa::kv4_decode_kernel<D, NT, kDtype, kScores><<<blocks, 128, S::kSmem, s>>>(p);
+  launch_after(sa::kv4_decode_kernel<D, NT, kDtype, kScores>, dim3(blocks), dim3(128), S::kSmem, s,
+               p);
   const int units = p.c.B * p.c.H * p.row_blocks;
   const int chunks = (p.c.N + sa::kJoinKeys - 1) / sa::kJoinKeys;
   // Long rows leave many partial results: a block merges one query row's. With 8 or
@@ -328,8 +329,8 @@ bool launch_chunk(const sa::Kv4AttendParams& p, cudaStream_t s) {
   using S = sa::ChunkShape<D>;
   if (!allow_smem<sa::kv4_chunk_kernel<D, kDtype>>(S::kSmem, 128)) return false;
   const int blocks = std::min(sm_count(), kMostSms);
-  sa::kv4_stage_kernel<D, kDtype>
-      <<<dim3(p.q_tiles + (p.add_weight ? 2 : 1), p.c.H, p.c.B), 256, 0, s>>>(p);
+  launch_after(sa::kv4_stage_kernel<D, kDtype>,
+               dim3(p.q_tiles + (p.add_weight ? 2 : 1), p.c.H, p.c.B), dim3(256), 0, s, p);
   const int pairs = std::max(blocks / 2, 1);
   launch_after(sa::kv4_chunk_kernel<D, kDtype>, dim3(2 * pairs), dim3(S::kThreads), S::kSmem, s,
                p);
@@ -370,13 +371,15 @@ cudaError_t launch_evict(sa::Kv4EvictParams p, cudaStream_t s) {
   cfg.blockDim = dim3(1024);
   cfg.dynamicSmemBytes = sa::kEvictFixedSmem + p.smem_keys * 4;
   cfg.stream = s;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = cluster;
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, sa::kv4_evict_kernel<D>, p);
 }
 
@@ -416,11 +419,13 @@ SA_API int sa_kv4_append(const sa_kv4_cache* c, const sa_rows* K, const sa_rows*
   const long long items = 1LL * T * (D / 16);
   const dim3 grid(static_cast<unsigned>(items > 0 ? (items + 255) / 256 : 1), p.c.H, p.c.B);
   if (D == 128)
-    dtype == SA_DTYPE_FP16 ? sa::kv4_append_kernel<128, SA_DTYPE_FP16><<<grid, 256, 0, s>>>(p)
-                           : sa::kv4_append_kernel<128, SA_DTYPE_BF16><<<grid, 256, 0, s>>>(p);
+    launch_after(dtype == SA_DTYPE_FP16 ? sa::kv4_append_kernel<128, SA_DTYPE_FP16>
+                                        : sa::kv4_append_kernel<128, SA_DTYPE_BF16>,
+                 grid, dim3(256), 0, s, p);
   else
-    dtype == SA_DTYPE_FP16 ? sa::kv4_append_kernel<64, SA_DTYPE_FP16><<<grid, 256, 0, s>>>(p)
-                           : sa::kv4_append_kernel<64, SA_DTYPE_BF16><<<grid, 256, 0, s>>>(p);
+    launch_after(dtype == SA_DTYPE_FP16 ? sa::kv4_append_kernel<64, SA_DTYPE_FP16>
+                                        : sa::kv4_append_kernel<64, SA_DTYPE_BF16>,
+                 grid, dim3(256), 0, s, p);
   return launched("append");
 }
 
@@ -444,11 +449,13 @@ SA_API int sa_kv4_read(const sa_kv4_cache* c, int first, const sa_rows* K, const
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const dim3 grid(static_cast<unsigned>((1LL * T * (D / 16) + 255) / 256), p.c.H, p.c.B);
   if (D == 128)
-    dtype == SA_DTYPE_FP16 ? sa::kv4_read_kernel<128, SA_DTYPE_FP16><<<grid, 256, 0, s>>>(p)
-                           : sa::kv4_read_kernel<128, SA_DTYPE_BF16><<<grid, 256, 0, s>>>(p);
+    launch_after(dtype == SA_DTYPE_FP16 ? sa::kv4_read_kernel<128, SA_DTYPE_FP16>
+                                        : sa::kv4_read_kernel<128, SA_DTYPE_BF16>,
+                 grid, dim3(256), 0, s, p);
   else
-    dtype == SA_DTYPE_FP16 ? sa::kv4_read_kernel<64, SA_DTYPE_FP16><<<grid, 256, 0, s>>>(p)
-                           : sa::kv4_read_kernel<64, SA_DTYPE_BF16><<<grid, 256, 0, s>>>(p);
+    launch_after(dtype == SA_DTYPE_FP16 ? sa::kv4_read_kernel<64, SA_DTYPE_FP16>
+                                        : sa::kv4_read_kernel<64, SA_DTYPE_BF16>,
+                 grid, dim3(256), 0, s, p);
   return launched("read");
 }
 

@@ -61,6 +61,7 @@ class QuantKVCache:
         b, h, n, half = codes.shape
         self.batch, self.kv_heads, self.capacity, self.head_dim = b, h, n, 2 * half
         self.device = codes.device
+        self._index = codes.device.index
         want = {"k_codes": (torch.uint8, (b, h, n, half)),
                 "v_codes": (torch.uint8, (b, h, n, half)),
                 "k_scales": (torch.uint8, (b, h, n, half // 8)),
@@ -107,8 +108,9 @@ class QuantKVCache:
         return counts.data_ptr()
 
     def _stream(self, stream):
-        s = torch.cuda.current_stream(self.device) if stream is None else stream
-        return s.cuda_stream
+        # the raw handle: making a Stream object costs more than the rest of a call's checks
+        return torch._C._cuda_getCurrentRawStream(self._index) if stream is None \
+            else stream.cuda_stream
 
     def _work(self, key, nbytes):
         """(pointer, bytes) of a workspace of at least `nbytes()`. One that became too small
