@@ -12,9 +12,9 @@
 // per pair, more than the product costs.
 //
 //  * Steps (key tile, query tile) are cut evenly over the blocks like the attention's.
-//  * warp 13 loads query tiles into a ring of four stages; warp 12 issues the products
-//    into the four tensor memory buffers of the same numbers; warpgroups 0 and 1 take
-//    every other step; warps 8-11 convert key tiles, one ahead.
+//  * One warp loads query tiles into a ring of four stages; one issues the products into
+//    the four tensor memory buffers of the same numbers; three warpgroups take the steps
+//    in turn; one converts key tiles, one ahead.
 #pragma once
 
 #include "kv4_chunk.cuh"
@@ -25,12 +25,13 @@ template <int D>
 struct WeightShape {
   static constexpr int kTile = 128 * D * 2;
   static constexpr int kStages = 4;
-  static constexpr int kThreads = 448;
+  static constexpr int kGroups = 3;  // warpgroups that take steps in turn
+  static constexpr int kThreads = 128 * (kGroups + 1) + 64;
   static constexpr int kOffK = 0;                              // two key tiles
   static constexpr int kOffQ = 2 * kTile;                      // query tiles
   static constexpr int kOffRow = kOffQ + kStages * kTile;      // [stage][scale | -lse][128]
-  static constexpr int kOffAcc = kOffRow + kStages * 1024;     // [2][128]
-  static constexpr int kOffBar = kOffAcc + 1024;
+  static constexpr int kOffAcc = kOffRow + kStages * 1024;     // [2][kGroups - 1][128]
+  static constexpr int kOffBar = kOffAcc + 1024 * (kGroups - 1);
   static constexpr int kSmem = kOffBar + 256 + 1024;           // + alignment slack
   static constexpr uint32_t kIdesc = ptx::idesc_f32acc(128, 128, 0, 0);
   __host__ __device__ static constexpr int QFULL(int s) { return s; }
@@ -43,7 +44,7 @@ struct WeightShape {
 };
 
 template <int D>
-__global__ void __launch_bounds__(448, 1)
+__global__ void __launch_bounds__(WeightShape<D>::kThreads, 1)
     kv4_weight_kernel(const __grid_constant__ Kv4AttendParams p) {
   using S = WeightShape<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -70,7 +71,8 @@ __global__ void __launch_bounds__(448, 1)
     *abort_flag = 0;
     ptx::fence_mbar_init();
   }
-  if (warp == 12) {
+  constexpr int kConvert = 4 * S::kGroups, kIssue = kConvert + 4;  // first warps of the roles
+  if (warp == kIssue) {
     ptx::tmem_alloc(ptx::smem_addr(tmem_slot), 512);
     ptx::tmem_relinquish();
   }
@@ -91,7 +93,7 @@ __global__ void __launch_bounds__(448, 1)
     return from + walk.t0;
   };
 
-  if (warp == 13) {
+  if (warp == kIssue + 1) {
     // -------------------------------------------------------------- query tiles
     if (lane == 0) {
       uint32_t step = 0;
@@ -121,7 +123,7 @@ __global__ void __launch_bounds__(448, 1)
       for (uint32_t k = step > S::kStages ? step - S::kStages : 0; k < step; ++k)
         ptx::mbar_wait(bar(S::QFULL(k % S::kStages)), (k / S::kStages) & 1, &none, c.status);
     }
-  } else if (warp == 12) {
+  } else if (warp == kIssue) {
     // -------------------------------------------------------------- MMA issuer
     // (the whole warp, for uniform values; see kv4_chunk_kernel)
     const bool issues = ptx_elect();
@@ -158,9 +160,9 @@ __global__ void __launch_bounds__(448, 1)
       ptx::umma_commit(bar(S::DRAIN()));
       ptx::mbar_wait(bar(S::DRAIN()), 0, &none, c.status);
     }
-  } else if (warp >= 8) {
+  } else if (warp >= kConvert) {
     // -------------------------------------------------------------- conversion
-    const int tid = threadIdx.x - 256;
+    const int tid = threadIdx.x - 32 * kConvert;
     uint32_t unit = 0;
     while (walk.next(p.weight_line)) {
       const int kb = unit & 1;
@@ -195,7 +197,7 @@ __global__ void __launch_bounds__(448, 1)
 #pragma unroll
       for (int a = 0; a < 8; ++a) acc[a] = 0.f;
       for (int t = 0; t < walk.t1 - walk.t0; ++t, ++step) {
-        if ((step & 1) != static_cast<uint32_t>(wg)) continue;
+        if (step % S::kGroups != static_cast<uint32_t>(wg)) continue;
         const int s = step % S::kStages;
         ok = ok && __all_sync(~0u, wait(S::SFULL(s), (step / S::kStages) & 1));
         if (!ok) continue;  // the barrier below is still met
@@ -244,11 +246,14 @@ __global__ void __launch_bounds__(448, 1)
       }
       const float sum = ((acc[0] + acc[1]) + (acc[2] + acc[3])) +
                         ((acc[4] + acc[5]) + (acc[6] + acc[7]));
-      // the two warpgroups' sums, always in the same order
-      if (wg == 1) s_acc[(unit & 1) * 128 + r] = sum;
-      asm volatile("bar.sync 1, 256;" ::: "memory");
+      // the warpgroups' sums, always in the same order
+      float* others = s_acc + (unit & 1) * (S::kGroups - 1) * 128 + r;
+      if (wg > 0) others[(wg - 1) * 128] = sum;
+      asm volatile("bar.sync 1, %0;" ::"n"(128 * S::kGroups) : "memory");
       if (wg == 0 && ok) {
-        const float both = sum + s_acc[(unit & 1) * 128 + r];
+        float both = sum;
+#pragma unroll
+        for (int k = 0; k < S::kGroups - 1; ++k) both += others[k * 128];
         if (walk.t0 > 0 || walk.t1 < walk.n) {
           p.part_w[partial_slot(blockIdx.x, walk.t0) * 128 + r] = both;
         } else if (j < held) {
@@ -263,7 +268,7 @@ __global__ void __launch_bounds__(448, 1)
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  if (warp == 12) ptx::tmem_dealloc(tmem, 512);
+  if (warp == kIssue) ptx::tmem_dealloc(tmem, 512);
 }
 
 // Weights of key tiles that lie in several blocks' ranges, summed in their order.
