@@ -244,8 +244,10 @@ AttendPlan plan_attend(const sa_kv4_cache* c, int heads, int T, bool weights) {
   a.few = rows <= kFewRows;
   size_t off = 0;
   if (a.few) {
-    a.nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
-    a.row_blocks = (rows + 8 * a.nt - 1) / (8 * a.nt);
+    // blocks of at most 32 query rows, as even as multiples of 8 allow
+    const int n8 = std::max((rows + 7) / 8, 1);
+    a.row_blocks = (n8 + 3) / 4;
+    a.nt = (n8 + a.row_blocks - 1) / a.row_blocks;
     a.blocks = static_cast<long long>(kMostSms) * decode_blocks_per_sm(a.nt);
     const size_t slots = a.blocks + planes * a.row_blocks;
     a.off_o = off;
@@ -320,8 +322,9 @@ bool launch_decode_nt(const sa::Kv4AttendParams& p, int nt, cudaStream_t s) {
   if (nt == 1)
     return p.add_weight ? launch_decode<D, 1, kDtype, true>(p, s)
                         : launch_decode<D, 1, kDtype, false>(p, s);
-  return nt == 2 ? launch_decode<D, 2, kDtype, false>(p, s)
-                 : launch_decode<D, 4, kDtype, false>(p, s);
+  return nt == 2   ? launch_decode<D, 2, kDtype, false>(p, s)
+         : nt == 3 ? launch_decode<D, 3, kDtype, false>(p, s)
+                   : launch_decode<D, 4, kDtype, false>(p, s);
 }
 
 template <int D, int kDtype>
