@@ -270,6 +270,44 @@ def test_attend_matches_the_oracle(shape, dtype):
     assert p.gpu.check() == sa.SA_OK
 
 
+@pytest.mark.parametrize("G,T", [(1, 8), (3, 3), (2, 8), (1, 17), (8, 3), (5, 5), (4, 8), (11, 3),
+                                 (8, 5), (7, 7), (16, 4), (5, 13)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attend_around_every_count_of_few_query_rows(G, T, D):
+    """Query rows from one block of 8 to two of 32 and just beyond, masked inside a tile."""
+    rows = [T + 3, 97, 161, 0, 64]
+    p = Pair(5, 2, D, 256, HF)
+    p.append(("few", G, T, D), 161, counts=rows)
+    counts = [T, T - 1, T, 0, 1]
+    e = p.check_attend(("few", G, T, D), T, 2 * G, counts=counts, causal=True, add_weight=True)
+    e = max(e, p.check_attend(("few2", G, T, D), T, 2 * G, add_weight=True, q_scale=2.0))
+    p.check_weights(2, e)
+
+
+@pytest.mark.parametrize("T", [1, 5, 70])
+def test_attend_many_sequences(T):
+    """More sequences than a warp has lanes, of every length from none to several tiles."""
+    B, H, G, D = 70, 2, 2, 64
+    p = Pair(B, H, D, 256)
+    lens = [(b * 37) % 200 for b in range(B)]
+    p.append(("many", T), 200, counts=lens)
+    counts = [min(T, n) if b % 3 else 0 for b, n in enumerate(lens)]
+    e = p.check_attend(("many", T), T, H * G, counts=counts, causal=True, add_weight=True)
+    p.check_weights(1, e)
+
+
+def test_attend_items_split_over_many_blocks():
+    """One head with a long cache: every block has a part of it, few and many query rows."""
+    H, D, n = 1, 128, 40_000
+    p = Pair(1, H, D, 40_064)
+    for i in range(4):
+        p.append(("split", i), n // 4)
+    e = 0.0
+    for T, G in ((1, 2), (6, 2), (40, 2), (300, 2)):
+        e = max(e, p.check_attend(("split", T), T, G, add_weight=True))
+    p.check_weights(4, e)
+
+
 @pytest.mark.parametrize("T", [1, 4, 90, 200])
 def test_attend_ragged_counts_leave_the_rest(T):
     B, H, G, D = 4, 2, 2, 128
@@ -452,6 +490,28 @@ def test_evict_matches_the_oracle(D, ties, n, keep, first, recent):
         check_evicted(p)
 
 
+@pytest.mark.parametrize("n,keep", [(8200, 8000), (20_000, 9_001), (33_000, 32_999)])
+@pytest.mark.parametrize("ties", [False, True])
+def test_evict_over_several_blocks(n, keep, ties):
+    """Heads shared by clusters of two to eight blocks, most weights equal or all distinct."""
+    H, D = 3, 64
+    c = sa.QuantKVCache(1, H, D, -(-n // 128) * 128)
+    g = torch.Generator(device="cuda").manual_seed(n)
+    K = torch.randn((1, n, H, D), generator=g, device="cuda").bfloat16()
+    c.append(K, K)
+    w = torch.randint(0, 2, c.weight.shape, generator=g, device="cuda").float() if ties else \
+        torch.rand(c.weight.shape, generator=g, device="cuda")
+    c.weight.copy_(w)
+    vc = c.v_codes.clone()
+    c.evict(keep, first=5, recent=100)
+    for h in range(H):
+        src = torch.tensor(kv4.rows_after_eviction(w[0, h, :n].cpu().numpy(), np.arange(n), n,
+                                                   keep, 5, 100), device="cuda")
+        assert torch.equal(c.weight[0, h, :keep], w[0, h, src])
+        assert torch.equal(c.v_codes[0, h, :keep], vc[0, h, src])
+        assert torch.equal(c.pos[0, h, :keep], src.int())
+
+
 def test_evict_leaves_shorter_sequences_and_rows_behind():
     p = Pair(3, 2, 64, 512)
     p.append("sh", 400, counts=[400, 0, 150])
@@ -575,6 +635,38 @@ def test_a_decoding_loop_captured_and_replayed():
         assert torch.equal(c.weight[b, :, :n], eager.weight[b, :, :n])
         assert torch.equal(c.k_codes[b, :, :n], eager.k_codes[b, :, :n])
     assert c.check() == sa.SA_OK
+
+
+def test_capture_needs_the_workspace_to_be_there():
+    p = Pair(1, 1, 64, 128)
+    p.append("cap", 10)
+    q = normal("capq", (1, 1, 1, 64), BF).cuda()
+    graph = torch.cuda.CUDAGraph()
+    with pytest.raises(RuntimeError, match="before capturing"):
+        with torch.cuda.graph(graph):
+            p.gpu.attend(q)
+    torch.cuda.synchronize()
+    out = p.gpu.attend(q)  # and the cache still works
+    assert torch.isfinite(out.float()).all()
+
+
+def test_a_larger_workspace_leaves_captured_graphs_theirs():
+    """A call that needs a larger workspace comes between a capture and its replay."""
+    p = Pair(1, 2, 64, 512)
+    p.append("wsp", 400)
+    q = normal("wspq", (1, 1, 4, 64), BF).cuda()
+    out = torch.empty_like(q)
+    p.gpu.attend(q, out=out)
+    want = out.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        p.gpu.attend(q, out=out)
+    big = normal("wspb", (1, 300, 4, 64), BF).cuda()
+    p.gpu.attend(big, add_weight=True)
+    junk = [torch.full((1 << 20,), float("nan"), device="cuda") for _ in range(8)]
+    out.zero_()
+    graph.replay()
+    assert torch.equal(out, want) and len(junk) == 8
 
 
 def test_calls_on_another_stream():
