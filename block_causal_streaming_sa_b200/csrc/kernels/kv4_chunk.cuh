@@ -219,16 +219,23 @@ __global__ void __launch_bounds__(256)
   if (static_cast<int>(blockIdx.x) >= p.q_tiles) {
     if (blockIdx.y != 0 || blockIdx.z != 0) return;
     if (static_cast<int>(blockIdx.x) == p.q_tiles) {
-      lay_line(p.line, c.B, c.H, [&](int b, int i) {
-        const int n_tok = tokens_of(p.counts, b, p.T);
-        if (i == 0) check_order(p, b, n_tok);
-        return item_tiles(p, rows_held(c, b), n_tok, i);
-      });
+      for (int b = threadIdx.x; b < c.B; b += 256)
+        check_order(p, b, tokens_of(p.counts, b, p.T));
+      lay_line(
+          p.line, c.B, c.H,
+          [&](int b) {
+            return (tokens_of(p.counts, b, p.T) * p.group + kItemRows - 1) / kItemRows;
+          },
+          [&](int b, int i) {
+            return item_tiles(p, rows_held(c, b), tokens_of(p.counts, b, p.T), i);
+          });
     } else {
-      lay_line(p.weight_line, c.B, c.H, [&](int b, int i) {
-        int from;
-        return weight_steps(p, rows_held(c, b), tokens_of(p.counts, b, p.T), i, from);
-      });
+      lay_line(
+          p.weight_line, c.B, c.H, [&](int b) { return (rows_held(c, b) + 127) / 128; },
+          [&](int b, int i) {
+            int from;
+            return weight_steps(p, rows_held(c, b), tokens_of(p.counts, b, p.T), i, from);
+          });
     }
     return;
   }
@@ -511,7 +518,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(512, 1)
       };
       constexpr std::integral_constant<int, 0> tile0;
       constexpr std::integral_constant<int, 1> tile1;
-      while (ok && walk.next(p.line)) {
+      while (ok && walk.next(p.line, c.B)) {
         const bool two = item_halves() == 2;
         const int t0 = __shfl_sync(~0u, walk.t0, 0), t1 = __shfl_sync(~0u, walk.t1, 0);
         int sk = 0, sv = 0;
@@ -561,7 +568,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(512, 1)
       uint32_t item = 0;
       bool ok = true;
       volatile int none = 0;
-      while (ok && walk.next(p.line)) {
+      while (ok && walk.next(p.line, c.B)) {
         const int q = item & 1, n_rows = tokens_of(p.counts, walk.b, p.T) * p.group;
         ok = wait(S::QEMPTY(q), ((item >> 1) & 1) ^ 1u);
         if (!ok) break;
@@ -622,7 +629,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(512, 1)
         return static_cast<uint32_t>(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
       });
     };
-    while (ok && walk.next(p.line)) {
+    while (ok && walk.next(p.line, c.B)) {
       const int held = rows_held(c, walk.b);
       const size_t plane = (static_cast<size_t>(walk.b) * c.H + walk.h) * c.N;
       ConvertRegs<N> kx, vx;
@@ -658,7 +665,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(512, 1)
     const uint32_t read = leader_addr(bar(S::READ(i))), p_full = leader_addr(bar(S::PFULL(i)));
     uint32_t s_phase = 0, items = 0;
     bool ok = true;
-    while (ok && walk.next(p.line)) {
+    while (ok && walk.next(p.line, c.B)) {
       const int held = rows_held(c, walk.b), n_tok = tokens_of(p.counts, walk.b, p.T);
       const int n_rows = n_tok * p.group;
       if (i >= item_halves()) continue;

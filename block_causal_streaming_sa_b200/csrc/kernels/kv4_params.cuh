@@ -43,8 +43,12 @@ __device__ __forceinline__ float score_factor(const float scale_log2, float row_
 // sequence have the same items.
 struct StepLine {
   long long* begin;  // [B + 1]: steps before sequence b
-  int* pre;          // [B][items + 1]: steps of one head of b before that item
-  int items;
+  int* pre;          // [B][items + 2]: steps of one head of b before each of its items and
+                     // after the last; at the end the number of its items
+  int items;         // at most
+  __device__ __forceinline__ int* row(int b) const {
+    return pre + static_cast<size_t>(b) * (items + 2);
+  }
 };
 
 // Query rows of one (sequence, KV head): row r is token r / group, query head
@@ -94,27 +98,29 @@ __device__ __forceinline__ float row_factor(float amax) {
   return __uint_as_float((254u - min(max(e, 1u), 253u)) << 23);
 }
 
-// Fills `line` from tiles(b, item), the steps of an item: one block of 256 threads, a
-// sequence per warp.
-template <typename F>
-__device__ __forceinline__ void lay_line(const StepLine& line, int B, int H, F tiles) {
+// Fills `line` from count(b), the items of sequence b, and steps(b, item): one block of
+// 256 threads, a sequence per warp.
+template <typename F, typename G>
+__device__ __forceinline__ void lay_line(const StepLine& line, int B, int H, F count, G steps) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int b = warp; b < B; b += 8) {
-    int* pre = line.pre + static_cast<size_t>(b) * (line.items + 1);
+    int* pre = line.row(b);
+    const int n = min(count(b), line.items);
     int sum = 0;
-    for (int i0 = 0; i0 < line.items; i0 += 32) {
-      const int v = i0 + lane < line.items ? tiles(b, i0 + lane) : 0;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      const int v = i0 + lane < n ? steps(b, i0 + lane) : 0;
       int x = v;
 #pragma unroll
       for (int k = 1; k < 32; k <<= 1) {
         const int y = __shfl_up_sync(~0u, x, k);
         if (lane >= k) x += y;
       }
-      if (i0 + lane < line.items) pre[i0 + lane] = sum + x - v;
+      if (i0 + lane < n) pre[i0 + lane] = sum + x - v;
       sum += __shfl_sync(~0u, x, 31);
     }
     if (lane == 0) {
-      pre[line.items] = sum;
+      pre[n] = sum;
+      pre[line.items + 1] = n;
       line.begin[b + 1] = static_cast<long long>(sum) * H;
     }
   }
@@ -146,16 +152,25 @@ struct LineWalk {
     stop = to;
     b = h = item = t0 = t1 = n = 0;
   }
-  // The next item of the range; false at its end.
-  __device__ __forceinline__ bool next(const StepLine& line) {
+  // The next item of the range of a line over B sequences; false at its end.
+  __device__ __forceinline__ bool next(const StepLine& line, int B) {
     if (at >= stop) return false;
-    while (at >= line.begin[b + 1]) ++b;
-    const int* pre = line.pre + static_cast<size_t>(b) * (line.items + 1);
-    const int per_head = pre[line.items];
+    int lo = b, hi = B;  // begin[lo] <= at < begin[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (line.begin[mid] <= at)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    b = lo;  // of sequences without steps that share a start, the last is the one with steps
+    const int* pre = line.row(b);
+    const int items = pre[line.items + 1], per_head = pre[items];
     const long long in_b = at - line.begin[b];
     h = static_cast<int>(in_b / per_head);
     const int in_h = static_cast<int>(in_b % per_head);
-    int lo = 0, hi = line.items;  // pre[lo] <= in_h < pre[hi]
+    lo = 0;
+    hi = items;  // pre[lo] <= in_h < pre[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
       if (pre[mid] <= in_h)
@@ -202,7 +217,7 @@ struct SplitItem {
     const long long from = (boundary + 1) * share;
     if (from >= total) return false;
     w.start(from, total);
-    w.next(line);
+    w.next(line, B);
     const long long begin = from - w.t0, end = begin + w.n;
     if (w.t0 == 0 || from - share > begin) return false;
     first = static_cast<int>(begin / share);

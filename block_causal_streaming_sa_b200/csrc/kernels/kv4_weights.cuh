@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(WeightShape<D>::kThreads, 1)
     if (lane == 0) {
       uint32_t step = 0;
       bool ok = true;
-      while (ok && walk.next(p.weight_line)) {
+      while (ok && walk.next(p.weight_line, c.B)) {
         const size_t tile0 = (static_cast<size_t>(walk.b) * c.H + walk.h) * p.q_tiles + first_tile();
         for (int t = 0; t < walk.t1 - walk.t0; ++t, ++step) {
           const int s = step % S::kStages;
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(WeightShape<D>::kThreads, 1)
     };
     uint32_t step = 0, unit = 0;
     bool ok = true;
-    while (ok && walk.next(p.weight_line)) {
+    while (ok && walk.next(p.weight_line, c.B)) {
       const int kb = unit & 1, steps = __shfl_sync(~0u, walk.t1 - walk.t0, 0);
       ok = all_wait(S::KFULL(kb), (unit >> 1) & 1);
       for (int t = 0; ok && t < steps; ++t, ++step) {
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(WeightShape<D>::kThreads, 1)
     // -------------------------------------------------------------- conversion
     const int tid = threadIdx.x - 32 * kConvert;
     uint32_t unit = 0;
-    while (walk.next(p.weight_line)) {
+    while (walk.next(p.weight_line, c.B)) {
       const int kb = unit & 1;
       const size_t row0 = (static_cast<size_t>(walk.b) * c.H + walk.h) * c.N +
                           static_cast<size_t>(walk.item) * 128;
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(WeightShape<D>::kThreads, 1)
     float* s_acc = reinterpret_cast<float*>(smem + S::kOffAcc);
     uint32_t step = 0, unit = 0;
     bool ok = true;
-    while (walk.next(p.weight_line)) {
+    while (walk.next(p.weight_line, c.B)) {
       const int held = rows_held(c, walk.b), n_tok = tokens_of(p.counts, walk.b, p.T);
       const int j = walk.item * 128 + r;
       // first query row that sees row j

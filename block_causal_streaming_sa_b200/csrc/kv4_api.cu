@@ -7,6 +7,7 @@
 #include <cmath>
 #include <initializer_list>
 #include <string>
+#include <utility>
 
 #include "host_common.h"
 #include "kernels/kv4_chunk.cuh"
@@ -111,9 +112,18 @@ int check_rows(const sa_rows* r, const char* name, int B, int T, int heads, int 
     if (s < 0 || s % 8 != 0)
       return refuse(SA_ERR_INVALID_ARG,
                     std::string(name) + ": strides must be multiples of 8 and >= 0");
-  if (written && ((B > 1 && r->stride_b < D) || (T > 1 && r->stride_t < D) ||
-                  (heads > 1 && r->stride_h < D)))
-    return refuse(SA_ERR_INVALID_ARG, std::string(name) + ": rows that are written overlap");
+  if (written) {
+    // from the smallest stride up, each has to step over all that lies below it
+    std::pair<int64_t, int> dim[3] = {{r->stride_b, B}, {r->stride_t, T}, {r->stride_h, heads}};
+    std::sort(dim, dim + 3);
+    int64_t span = D;
+    for (const auto& d : dim) {
+      if (d.second <= 1) continue;
+      if (d.first < span)
+        return refuse(SA_ERR_INVALID_ARG, std::string(name) + ": rows that are written overlap");
+      span += d.first * (d.second - 1);
+    }
+  }
   std::string why;
   if (!device_memory(r->data, device, name, &why)) return refuse(SA_ERR_INVALID_ARG, why);
   out->data = r->data;
@@ -275,7 +285,7 @@ AttendPlan plan_attend(const sa_kv4_cache* c, int heads, int T, bool weights) {
     const int items[2] = {a.items, c->capacity / 128};
     for (int i = 0; i < (weights ? 2 : 1); ++i) {
       a.off_begin[i] = take((c->batch + 1) * sizeof(long long));
-      a.off_pre[i] = take(static_cast<size_t>(c->batch) * (items[i] + 1) * sizeof(int));
+      a.off_pre[i] = take(static_cast<size_t>(c->batch) * (items[i] + 2) * sizeof(int));
     }
     if (weights) a.off_w = take(2ull * kMostSms * 128 * sizeof(float));
     // two partial results of 512 rows a pair of SMs

@@ -468,7 +468,9 @@ typedef struct {
 
 /* Rows of [B, T, heads, D] in device memory: value (b, t, h, d) is element
  * b * stride_b + t * stride_t + h * stride_h + d of data (16-byte aligned, strides
- * multiples of 8 and >= 0), so a slice of a fused projection can be passed. */
+ * multiples of 8 and >= 0), so a slice of a fused projection can be passed. Rows that
+ * a call writes must lie apart: in order of size, each stride of an extent above 1
+ * must step over all rows below it. */
 typedef struct {
   void* data;
   int64_t stride_b, stride_t, stride_h;
@@ -563,7 +565,8 @@ SA_API const char* sa_last_error(const sa_handle* h);
  * size of its buffer before making it; an access past the end is skipped and
  * recorded in the device status word (sa_get_status -> SA_ERR_BOUNDS). A
  * debugging aid in place of a memory checker; the release build (libsa.so)
- * has no checks. Host only. */
+ * has no checks. The 4-bit cache's kernels are the same in both: they clamp the
+ * numbers of rows they read from device memory to the capacity. Host only. */
 #define SA_BUILD_DEVICE_CHECKS 1
 SA_API int sa_build_info(void);
 

@@ -719,6 +719,8 @@ def test_refusals_launch_nothing():
     bad(inv, sa.sa_kv4_read, c, -2, rows, orow, 0, 3)
     bad(inv, sa.sa_kv4_read, c, 0, rows, rows, 0, 3)
     bad(inv, sa.sa_kv4_read, c, 0, sa.SaRows(x.data_ptr(), 384, 0, 64), orow, 0, 3)
+    bad(inv, sa.sa_kv4_read, c, 0, sa.SaRows(x.data_ptr(), 384, 64, 64), orow, 0, 3)
+    bad(inv, sa.sa_kv4_read, c, 0, sa.SaRows(x.data_ptr(), 320, 128, 64), orow, 0, 3)
     bad(inv, sa.sa_kv4_attend, c, rows, orow, 0, 3, 3, **full)   # heads % kv_heads
     bad(inv, sa.sa_kv4_attend, c, rows, rows, 0, 2, 3, **full)   # O aliases Q
     bad(inv, sa.sa_kv4_attend, c, rows, orow, 0, 2, 3, scale=float("nan"), **full)
