@@ -1,6 +1,7 @@
-"""Fit of the polynomial behind ptx::exp2_poly (kernels/ptx.cuh).
+"""Fit of the polynomials behind ptx::exp2_poly (kernels/ptx.cuh, degree 3) and
+exp2_fma2 (kernels/kv4_params.cuh, degree 5).
 
-2^f on [-1/2, 1/2] by a degree-3 polynomial, minimax in relative error, found
+2^f on [-1/2, 1/2] by a polynomial, minimax in relative error, found
 with the Remez exchange algorithm (equioscillation of the relative error at
 deg + 2 reference points, reference moved to the error's extrema each pass).
 Prints the coefficients (float32) and the max relative error of the float32
@@ -48,9 +49,10 @@ def horner32(c, t):
 
 
 if __name__ == "__main__":
-    c = remez(3)
     t = np.linspace(-0.5, 0.5, 100001).astype(np.float32)
     ref = np.exp2(t.astype(np.float64))
-    err = np.max(np.abs(horner32(c, t) - ref) / ref)
-    print("coefficients c0..c3:", [float(np.float32(v)) for v in c])
-    print(f"max relative error (float32 Horner): {err:.3e}")
+    for deg in (3, 5):
+        c = remez(deg)
+        err = np.max(np.abs(horner32(c, t) - ref) / ref)
+        print(f"coefficients c0..c{deg}:", [float(np.float32(v)) for v in c])
+        print(f"max relative error (float32 Horner): {err:.3e}")

@@ -13,19 +13,23 @@
 //    codes of one aligned 16-byte (D = 64: 8-byte) piece of a row, in order.
 //  * O^T = V^T P^T: 16 values x 8 query rows x 16 cache rows. A lane owns D / 8
 //    consecutive values of four rows; two rows' codes are merged into bytes before
-//    the conversion, which then yields pairs of rows. P^T comes from S^T by transposing 8 x 8 blocks
-//    (movmatrix); both keep query rows on the same lanes, so the softmax statistics
-//    never move.
+//    the conversion, which then yields pairs of rows. P^T comes from S^T by
+//    transposing 8 x 8 blocks (movmatrix); both keep query rows on the same lanes, so
+//    the softmax statistics never move.
 //  * The running maximum of a query row is raised only when a score exceeds it by
 //    more than 2^8 (checked by one vote a tile): no reduction across lanes otherwise.
 //    P stays below 2^8 and l and O are fp32.
-//  * Each warp streams tiles of 32 rows through a ring of its own (bulk copies by
-//    its lane 0, an mbarrier a stage), so warps never wait for one another.
+//  * Each warp streams tiles of 32 rows through a ring of its own (a bulk copy by
+//    each of four lanes, an mbarrier a stage), so warps never wait for one another.
 //  * The rows of all sequences and heads are one line of tiles, cut into equal
 //    ranges, one a block, whatever the lengths: long rows are split over blocks and
 //    short ones share one. A range that crosses heads leaves one partial result per
 //    head; (block + head) numbers them without gaps growing beyond blocks + heads.
 //    kv4_join_kernel merges them in that order.
+//
+// Measured: 4 x 131071 rows, 8 heads, D 128, 8 query rows: 125 us, 4.8 TB/s (the copies
+// alone, without arithmetic, 91 us; the rest is unpacking at the 1.3 GHz held under
+// this load). 700 rows, 8 heads: 10 us, launches and dependent loads.
 #pragma once
 
 #include "kv4_params.cuh"

@@ -18,6 +18,9 @@
 //    the warps and arithmetic give the places of its holes and movers;
 //  * the j-th hole takes the j-th mover. Writes go below `keep`, reads come from `keep`
 //    on, so the moves need no order among themselves.
+//
+// Measured: 54000 rows down to 43200, 12 heads, D 128: 25 to 33 us; one row of 4097, 64
+// heads: 16 us (a first version, a block a head and a launch for the moves: 280 and 45).
 #pragma once
 
 #include <cooperative_groups.h>

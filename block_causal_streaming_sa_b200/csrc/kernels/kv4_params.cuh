@@ -17,8 +17,8 @@ __device__ __forceinline__ void exp2_fma2(float& y0, float& y1, float x0, float 
   constexpr float c0 = 1.0000001192092896f, c1 = 0.6931469440460205f, c2 = 0.24022120237350464f;
   constexpr float c3 = 0.05550713092088699f, c4 = 0.009675540961325169f;
   constexpr float c5 = 0.0013276472454890609f;
-  x0 = fmaxf(x0, -127.0f);
-  x1 = fmaxf(x1, -127.0f);
+  asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x0));  // -127; a NaN stays one
+  asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x1));
   float t0, t1, f0, f1, q0, q1;
   ptx::fadd2(t0, t1, x0, x1, kRound, kRound);
   ptx::fadd2(f0, f1, t0, t1, -kRound, -kRound);  // n
