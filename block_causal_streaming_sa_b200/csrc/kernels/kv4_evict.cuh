@@ -25,6 +25,8 @@
 
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "kv4_format.cuh"
 
 namespace sa {
@@ -72,6 +74,21 @@ __global__ void __launch_bounds__(1024, 1)
   wait_for_previous();
   const int n = rows_held(c, b);
   const size_t plane = (static_cast<size_t>(b) * c.H + h) * c.N;
+
+  // A barrier of all of the head's blocks (the cluster's takes 1500 cycles even for one).
+  auto sync_head = [&]() {
+    if (blocks > 1)
+      cluster.sync();
+    else
+      __syncthreads();
+  };
+  // Sum over the head's blocks of their copies of a counter.
+  auto sum_over_blocks = [&](const int* mine) {
+    if (blocks == 1) return *mine;
+    int sum = 0;
+    for (int r = 0; r < blocks; ++r) sum += *cluster.map_shared_rank(mine, r);
+    return sum;
+  };
 
   // The warps' ordered scan of a pair of counts (low and high word): the sum over lower
   // warps, and the block's total. `buffer`: 0 and 1 in turn, so one barrier does.
@@ -134,8 +151,7 @@ __global__ void __launch_bounds__(1024, 1)
         if (pass == 0 || k >> above == prefix) atomicAdd(&count[(k >> shift) & 2047u], 1);
       }
       __syncthreads();
-      const int per = pass == 0 ? 32 : 64;  // bins of a coarse sum, one sum a warp
-      int sum = 0;
+      int sum = 0;  // of 32 (64) bins, one sum a warp
       if (pass == 0) {
 #pragma unroll
         for (int k = 0; k < kEvictCopies; ++k) sum += copies[k * 1024 + threadIdx.x];
@@ -146,32 +162,37 @@ __global__ void __launch_bounds__(1024, 1)
 #pragma unroll
       for (int k = 16; k; k >>= 1) sum += __shfl_xor_sync(~0u, sum, k);
       if (lane == 0) coarse[pass * 32 + warp] = sum;
-      cluster.sync();
+      sync_head();
       if (warp == 0) {
-        // Counts from the top, one of `width` neighbours a lane: the lane in which the
-        // left-th row from the top lies.
+        // Counts from the top, `PER` bins a lane: the bin in which the left-th row from the
+        // top lies, and how many of it are wanted.
         int need = left;
-        auto search = [&](const int* sums, int from, int width) {
-          const int i = from + width - 1 - lane;
-          int v = 0;
-          if (lane < width)
-            for (int r = 0; r < blocks; ++r) v += cluster.map_shared_rank(sums, r)[i];
-          int x = v;
+        auto search = [&](const int* counts, int from, auto per_lane) {
+          constexpr int PER = decltype(per_lane)::value;
+          int v[PER], x = 0;
+          const int top = from + 32 * PER - 1 - lane * PER;
+#pragma unroll
+          for (int k = 0; k < PER; ++k) x += v[k] = sum_over_blocks(counts + top - k);
+          const int own = x;
 #pragma unroll
           for (int k = 1; k < 32; k <<= 1) {
             const int y = __shfl_up_sync(~0u, x, k);
             if (lane >= k) x += y;
           }
-          const unsigned enough = __ballot_sync(~0u, x >= need);
-          const int at = enough ? __ffs(enough) - 1 : -1;  // -1: not among these
-          const int before = __shfl_sync(~0u, x - v, at < 0 ? 31 : at);
-          const int all = __shfl_sync(~0u, x, 31);
-          need -= at < 0 ? all : before;
-          return at < 0 ? -1 : from + width - 1 - at;
+          // (there are at least `need` rows: some lane reaches it)
+          const int at = max(__ffs(__ballot_sync(~0u, x >= need)) - 1, 0);
+          int bin = top, rest = need - (x - own);
+          if (PER == 2 && rest > v[0]) {
+            bin = top - 1;
+            rest -= v[0];
+          }
+          need = __shfl_sync(~0u, rest, at);
+          return __shfl_sync(~0u, bin, at);
         };
-        const int block = search(coarse + pass * 32, 0, 32);
-        int bin = search(mine, (block + 1) * per - 32, 32);
-        if (bin < 0) bin = search(mine, block * per, 32);
+        constexpr std::integral_constant<int, 1> one;
+        constexpr std::integral_constant<int, 2> two;
+        const int block = search(coarse + pass * 32, 0, one);
+        const int bin = pass == 0 ? search(mine, block * 32, one) : search(mine, block * 64, two);
         if (lane == 0) {
           s_pick[0] = bin;
           s_pick[1] = need;
@@ -184,7 +205,7 @@ __global__ void __launch_bounds__(1024, 1)
     // prefix: the keep-th largest key; the first `left` rows that equal it stay.
     int equal_before = 0;  // such rows in lower blocks: their last histograms tell
     for (int r = 0; r < rank; ++r)
-      equal_before += cluster.map_shared_rank(hist + 3072, r)[prefix & 2047u];
+      equal_before += *cluster.map_shared_rank(hist + 3072 + (prefix & 2047u), r);
     int more[2] = {0, 0}, equal[2] = {0, 0};  // below `keep` and from it on
     for (int j = j0; j < j1; j += 32) {
       const bool in = j + lane < j1;
@@ -211,15 +232,18 @@ __global__ void __launch_bounds__(1024, 1)
       s_pick[2] = static_cast<int>(total);
       s_pick[3] = static_cast<int>(total >> 32);
     }
-    cluster.sync();
-    int moves = 0;
-    for (int r = 0; r < blocks; ++r) {
-      const int* other = cluster.map_shared_rank(s_pick, r);
-      if (r < rank) {
-        holes += other[2];
-        movers += other[3];
+    sync_head();
+    int moves = s_pick[3];
+    if (blocks > 1) {
+      moves = 0;
+      for (int r = 0; r < blocks; ++r) {
+        const int* other = cluster.map_shared_rank(s_pick, r);
+        if (r < rank) {
+          holes += other[2];
+          movers += other[3];
+        }
+        moves += other[3];
       }
-      moves += other[3];
     }
     int32_t* hole_list = p.lists + plane;
     int32_t* mover_list = hole_list + c.N / 2;
@@ -240,7 +264,7 @@ __global__ void __launch_bounds__(1024, 1)
         movers += __popc(mover);
       }
     }
-    cluster.sync();  // lists written; no block reads another's shared memory from here
+    sync_head();  // lists written; no block reads another's shared memory from here
 
     // 16 threads a row: 16-byte pieces of codes, 4-byte ones of scales, position and
     // weight; four rows of each under way at a time.
