@@ -246,7 +246,8 @@ __global__ void __launch_bounds__(256)
   const int held = rows_held(c, b), n_tok = tokens_of(p.counts, b, p.T);
   const int n_rows = n_tok * p.group;
   if (tile * 128 >= n_rows) return;
-  const bool empty = item_tiles(p, held, n_tok, tile * 128 / kItemRows) == 0;  // no block goes there
+  // no block goes to an item without tiles
+  const bool empty = item_tiles(p, held, n_tok, tile * 128 / kItemRows) == 0;
   const size_t tile_id = (static_cast<size_t>(b) * c.H + h) * p.q_tiles + tile;
   uint8_t* dst = p.q_img + tile_id * (128 * D * 2);
   for (int i = threadIdx.x; i < 128 * C; i += 256) {
@@ -254,9 +255,8 @@ __global__ void __launch_bounds__(256)
     const int t = row / p.group, hq = h * p.group + row % p.group;
     uint4 w = make_uint4(0u, 0u, 0u, 0u);
     if (row < n_rows)
-      w = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q.data) +
-                                               b * p.q.sb + t * p.q.st + hq * p.q.sh) +
-                piece);
+      w = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q.data) + b * p.q.sb +
+                                         t * p.q.st + hq * p.q.sh)[piece];
     const float2 v[4] = {unpack2<kDtype>(w.x), unpack2<kDtype>(w.y), unpack2<kDtype>(w.z),
                          unpack2<kDtype>(w.w)};
     float amax = 0.f;
@@ -269,7 +269,8 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int k = 0; k < 4; ++k) x[k] = pack2<SA_DTYPE_FP16>(v[k].x * f, v[k].y * f);
     *reinterpret_cast<uint4*>(dst + tile_offset(r, piece)) = make_uint4(x[0], x[1], x[2], x[3]);
-    if (piece == 0) p.row_scale[tile_id * 128 + r] = row < n_rows ? score_factor(p.scale_log2, f) : 0.f;
+    if (piece == 0)
+      p.row_scale[tile_id * 128 + r] = row < n_rows ? score_factor(p.scale_log2, f) : 0.f;
     if (row >= n_rows) {
       if (piece == 0) p.row_nlse[tile_id * 128 + r] = -INFINITY;  // such rows draw no weight
     } else if (empty) {
@@ -380,8 +381,8 @@ __device__ __forceinline__ void convert_load(ConvertRegs<N>& x, const uint8_t* c
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const int row = (i * 128 + tid) / P, piece = (i * 128 + tid) % P;
-    x.w[i] = __ldg(src + key(row) * (D / 32) + piece);
-    x.sc[i] = __ldg(sc + key(row) * (D / 32) + piece);
+    x.w[i] = src[key(row) * (D / 32) + piece];
+    x.sc[i] = sc[key(row) * (D / 32) + piece];
   }
 }
 
@@ -837,7 +838,8 @@ __global__ void __launch_bounds__(128)
   const int row = w.item * kItemRows + r;
   if (row >= n_rows) return;
   float mx = -INFINITY;
-  for (int k = split.first; k <= split.last; ++k) mx = fmaxf(mx, p.part_ml[split.slot(k) * kItemRows + r].x);
+  for (int k = split.first; k <= split.last; ++k)
+    mx = fmaxf(mx, p.part_ml[split.slot(k) * kItemRows + r].x);
   const float ref = mx == -INFINITY ? 0.f : mx;
   float sum = 0.f;
   constexpr int V = D / 16;  // float4 of a thread
@@ -849,8 +851,8 @@ __global__ void __launch_bounds__(128)
     const float2 ml = p.part_ml[slot * kItemRows + r];
     const float a = ptx::ex2(ml.x - ref);
     sum += ml.y * a;
-    const float4* src =
-        reinterpret_cast<const float4*>(p.part_o) + slot * (D / 4) * kItemRows + part * V * kItemRows + r;
+    const float4* src = reinterpret_cast<const float4*>(p.part_o) +
+                        slot * (D / 4) * kItemRows + part * V * kItemRows + r;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const float4 x = src[j * kItemRows];

@@ -220,7 +220,7 @@ __device__ __forceinline__ void load_query(const Kv4AttendParams& p, int b, int 
                       (row / p.group) * p.q.st + (h * p.group + row % p.group) * p.q.sh +
                       tig * (D / 4);
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(q) + i);
+  for (int i = 0; i < D / 32; ++i) w[i] = reinterpret_cast<const uint4*>(q)[i];
 }
 
 // A warp tile's K codes as operand registers: [word][16-row half][rows g, g + 8][pair].
@@ -285,8 +285,10 @@ __global__ void __launch_bounds__(128, DecodeShape<D, NT>::kBlocksPerSm)
     ptx::fence_mbar_init();
   }
   __syncthreads();
-  begin_early();
+  // In this order: the join reads the lengths before it waits for this kernel, so it
+  // must not begin before the kernel that wrote them (an append) has finished.
   wait_for_previous();
+  begin_early();
 
   const Line line = line_of(p, gridDim.x, S::kTile, lane);
   int at = min(static_cast<long long>(blockIdx.x) * line.share,
@@ -331,8 +333,8 @@ __global__ void __launch_bounds__(128, DecodeShape<D, NT>::kBlocksPerSm)
       if (lane == 0) ptx::mbar_arrive_expect_tx(bar, S::kStageBytes);
       __syncwarp();
       if (lane < 4)
-        bulk_load(ring + stage * S::kStageBytes + copy_at, src + static_cast<size_t>(tile) * copy_bytes,
-                  copy_bytes, bar);
+        bulk_load(ring + stage * S::kStageBytes + copy_at,
+                  src + static_cast<size_t>(tile) * copy_bytes, copy_bytes, bar);
     };
     // The query row of this lane is asked for before the ring is filled: behind 200 KB of
     // copies an SM it would come microseconds later. Warps share the rows of NT > 1.
@@ -647,7 +649,9 @@ __global__ void __launch_bounds__(128)
   const int id = joins ? blockIdx.x / kGroups : (blockIdx.x - join_blocks) / chunks;
   const int units_b = c.H * p.row_blocks;
   const int b = joins ? id / units_b : id / c.H;
-  // lengths were there before the decode kernel began: the schedule needs no wait
+  // The lengths were there before the decode kernel let this one begin: the schedule
+  // needs no wait, only that this SM's L1 holds no older ones.
+  __threadfence();
   const int held = rows_held(c, b), n_tok = tokens_of(p.counts, b, p.T);
   const int n_rows = n_tok * p.group;
   const Line line = line_of(p, blocks, 32, lane);
@@ -754,8 +758,9 @@ __global__ void __launch_bounds__(128)
     uint16_t* dst = static_cast<uint16_t*>(p.o.data) + b * p.o.sb + t * p.o.st + hq * p.o.sh +
                     lane * V;
     if constexpr (V == 4)
-      *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<kDtype>(acc[0] * inv, acc[1] * inv),
-                                                  pack2<kDtype>(acc[V - 2] * inv, acc[V - 1] * inv));
+      *reinterpret_cast<uint2*>(dst) =
+          make_uint2(pack2<kDtype>(acc[0] * inv, acc[1] * inv),
+                     pack2<kDtype>(acc[V - 2] * inv, acc[V - 1] * inv));
     else
       *reinterpret_cast<uint32_t*>(dst) = pack2<kDtype>(acc[0] * inv, acc[1] * inv);
     if (lane == 0) {
@@ -844,6 +849,7 @@ __global__ void __launch_bounds__(128, 4)
     ptx::fence_mbar_init();
   }
   __syncthreads();
+  __threadfence();  // the lengths: as in the join
   const Line line = line_of(p, gridDim.x, S::kTile, lane);
   int at = min(static_cast<long long>(blockIdx.x) * line.share,
                static_cast<long long>(line.total));

@@ -20,7 +20,7 @@
 //    on, so the moves need no order among themselves.
 //
 // Measured: 54000 rows down to 43200, 12 heads, D 128: 25 to 33 us; one row of 4097, 64
-// heads: 16 us (a first version, a block a head and a launch for the moves: 280 and 45).
+// heads: 12 us (a first version, a block a head and a launch for the moves: 280 and 45).
 #pragma once
 
 #include <cooperative_groups.h>
@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(1024, 1)
     const int j0 = min((rank * 32 + warp) * per_warp, n);
     const int j1 = min(j0 + per_warp, n);
     auto compute_key = [&](int j) {
-      return evict_key(__ldg(c.weight + plane + j), __ldg(c.pos + plane + j), p.first, keep_from);
+      return evict_key(c.weight[plane + j], c.pos[plane + j], p.first, keep_from);
     };
     const int slot0 = warp * per_warp - j0;  // key slot of row j: slot0 + j
     auto key_of = [&](int j) {
@@ -127,8 +127,8 @@ __global__ void __launch_bounds__(1024, 1)
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         if (j + 32 * k < in_smem) {
-          w[k] = __ldg(c.weight + plane + j + 32 * k);
-          at[k] = __ldg(c.pos + plane + j + 32 * k);
+          w[k] = c.weight[plane + j + 32 * k];
+          at[k] = c.pos[plane + j + 32 * k];
         }
 #pragma unroll
       for (int k = 0; k < 4; ++k)

@@ -73,7 +73,8 @@ __device__ __forceinline__ void quantise_block(const uint4 (&in)[2], uint2* code
 // grid: (ceil(T * D / 16 / 256), H, B). The last block to finish moves seq on;
 // every block has read it by then.
 template <int D, int kDtype>
-__global__ void __launch_bounds__(256) kv4_append_kernel(const __grid_constant__ Kv4AppendParams p) {
+__global__ void __launch_bounds__(256)
+    kv4_append_kernel(const __grid_constant__ Kv4AppendParams p) {
   constexpr int NB = D / 16;
   const Kv4& c = p.c;
   const int b = blockIdx.z, h = blockIdx.y;
@@ -93,10 +94,10 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const __grid_constant__
                          h * p.k.sh + blk * 16;
     const uint16_t* vs = static_cast<const uint16_t*>(p.v.data) + b * p.v.sb + t * p.v.st +
                          h * p.v.sh + blk * 16;
-    kin[0] = __ldg(reinterpret_cast<const uint4*>(ks));
-    kin[1] = __ldg(reinterpret_cast<const uint4*>(ks) + 1);
-    vin[0] = __ldg(reinterpret_cast<const uint4*>(vs));
-    vin[1] = __ldg(reinterpret_cast<const uint4*>(vs) + 1);
+    kin[0] = __ldcg(reinterpret_cast<const uint4*>(ks));
+    kin[1] = __ldcg(reinterpret_cast<const uint4*>(ks) + 1);
+    vin[0] = __ldcg(reinterpret_cast<const uint4*>(vs));
+    vin[1] = __ldcg(reinterpret_cast<const uint4*>(vs) + 1);
     const size_t row = (static_cast<size_t>(b) * c.H + h) * c.N + base + t;
     quantise_block<kDtype>(kin, reinterpret_cast<uint2*>(c.k_codes + row * (D / 2)) + blk,
                            c.k_scales + row * NB + blk, bad);
@@ -177,8 +178,8 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(const __grid_constant__ K
   const int t = static_cast<int>(item / NB), blk = static_cast<int>(item % NB);
   if (t >= n || t >= held - base) return;
   const size_t row = (static_cast<size_t>(b) * c.H + h) * c.N + base + t;
-  const uint2 kc = __ldg(reinterpret_cast<const uint2*>(c.k_codes + row * (D / 2)) + blk);
-  const uint2 vc = __ldg(reinterpret_cast<const uint2*>(c.v_codes + row * (D / 2)) + blk);
+  const uint2 kc = reinterpret_cast<const uint2*>(c.k_codes + row * (D / 2))[blk];
+  const uint2 vc = reinterpret_cast<const uint2*>(c.v_codes + row * (D / 2))[blk];
   const unsigned ks = c.k_scales[row * NB + blk], vs = c.v_scales[row * NB + blk];
   dequantise_block<kDtype>(
       kc, ks,

@@ -102,7 +102,8 @@ __global__ void __launch_bounds__(WeightShape<D>::kThreads, 1)
       uint32_t step = 0;
       bool ok = true;
       while (ok && walk.next(p.weight_line, c.B)) {
-        const size_t tile0 = (static_cast<size_t>(walk.b) * c.H + walk.h) * p.q_tiles + first_tile();
+        const size_t tile0 =
+            (static_cast<size_t>(walk.b) * c.H + walk.h) * p.q_tiles + first_tile();
         for (int t = 0; t < walk.t1 - walk.t0; ++t, ++step) {
           const int s = step % S::kStages;
           ok = wait(S::EMPTY(s), ((step / S::kStages) & 1) ^ 1u);

@@ -458,7 +458,8 @@ typedef struct {
   uint8_t* k_scales;  /* [B, Hk, N, D / 16] */
   uint8_t* v_scales;  /* [B, Hk, N, D / 16] */
   int32_t* pos;       /* [B, Hk, N]: place of the row in its sequence, counted from
-                         0 over all rows ever appended */
+                         0 over all rows ever appended (less than 2^31 a sequence
+                         between resets) */
   float* weight;      /* [B, Hk, N]: attention weight the row has drawn */
   int32_t* seq;       /* [4, B]: rows held; rows appended in all; rows of the last
                          append (0 after an eviction); rows appended since the last

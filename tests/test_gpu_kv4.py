@@ -686,6 +686,37 @@ def test_calls_on_another_stream():
     assert p.gpu.seq[0].tolist() == [20]
 
 
+@pytest.mark.parametrize("T", [1, 12, 200])
+def test_lengths_are_those_behind_a_long_append(T):
+    """Kernels may begin while the ones in front of them run: a sequence of calls without a
+    pause gives the bits it gives with a wait after each."""
+    H, D, rows = 12, 128, 9000
+    g = torch.Generator(device="cuda").manual_seed(T)
+    K = torch.randn((2, rows, H, D), generator=g, device="cuda").bfloat16()
+    Q = torch.randn((2, T, H, D), generator=g, device="cuda").bfloat16()
+    counts = torch.tensor([rows, 217], dtype=torch.int32, device="cuda")
+
+    def run(pause):
+        c = sa.QuantKVCache(2, H, D, 36096)
+        results = []
+        for i in range(4):
+            c.append(K, K, counts=counts)
+            pause()
+            lse = torch.empty((2, H, T), device="cuda")
+            results += [c.attend(Q, causal=True, lse=lse, add_weight=True), lse]
+            pause()
+        c.evict(11_000, 16, 500)
+        pause()
+        results.append(c.attend(Q, add_weight=True))
+        assert c.check() == sa.SA_OK
+        return results + [c.weight[1, :, :868], c.weight[0, :, :11_000], c.pos[0, :, :11_000]]
+
+    run(torch.cuda.synchronize)  # workspaces and modules are there
+    want = run(torch.cuda.synchronize)
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(run(lambda: None), want))
+
+
 # ------------------------------------------------------------------ refusals
 
 def test_refusals_launch_nothing():
