@@ -249,6 +249,7 @@ int decode_blocks_per_sm(int nt) { return nt == 1 ? 4 : nt == 2 ? 3 : 2; }
 
 AttendPlan plan_attend(const sa_kv4_cache* c, int heads, int T, bool weights) {
   AttendPlan a{};
+  if (T == 0) return a;  // nothing runs
   const int rows = heads / c->kv_heads * T, D = c->head_dim;
   const size_t planes = static_cast<size_t>(c->batch) * c->kv_heads;
   a.few = rows <= kFewRows;
