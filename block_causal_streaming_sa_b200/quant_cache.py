@@ -61,6 +61,8 @@ class QuantKVCache:
         b, h, n, half = codes.shape
         self.batch, self.kv_heads, self.capacity, self.head_dim = b, h, n, 2 * half
         self.device = codes.device
+        if self.device.type != "cuda":
+            raise ValueError(f"the cache must be on a GPU, not on {self.device}")
         self._index = codes.device.index
         want = {"k_codes": (torch.uint8, (b, h, n, half)),
                 "v_codes": (torch.uint8, (b, h, n, half)),
@@ -112,7 +114,12 @@ class QuantKVCache:
         return torch._C._cuda_getCurrentRawStream(self._index) if stream is None \
             else stream.cuda_stream
 
-    def _work(self, key, nbytes):
+    def _empty(self, shape, dtype, stream):
+        # memory of the stream that writes it: another's may still be in use there
+        with torch.cuda.device(self.device), torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def _work(self, key, nbytes, stream):
         """(pointer, bytes) of a workspace of at least `nbytes()`. One that became too small
         stays allocated: a captured graph, or a call under way on another stream, may use it.
         Each is at least twice the one before, so all together are less than twice the last."""
@@ -124,9 +131,7 @@ class QuantKVCache:
             if torch.cuda.is_current_stream_capturing():
                 raise RuntimeError("make one call of this shape before capturing it: the "
                                    "workspace is too small")
-            with torch.cuda.device(self.device):
-                self._workspaces.append(torch.empty(max(need, 2 * have), dtype=torch.uint8,
-                                                    device=self.device))
+            self._workspaces.append(self._empty(max(need, 2 * have), torch.uint8, stream))
         last = self._workspaces[-1]
         return last.data_ptr(), last.numel()
 
@@ -161,7 +166,8 @@ class QuantKVCache:
         if heads < 1 or heads % self.kv_heads:
             raise ValueError(f"Q must have a multiple of {self.kv_heads} heads")
         if out is None:
-            out = torch.empty(Q.shape, dtype=Q.dtype, device=self.device)
+            out = self._empty(Q.shape, Q.dtype, stream) if stream is not None \
+                else torch.empty(Q.shape, dtype=Q.dtype, device=self.device)
         q = self._rows(Q, "Q", tokens, heads, Q.dtype)
         o = self._rows(out, "out", tokens, heads, Q.dtype)
         lse_ptr = 0
@@ -172,7 +178,8 @@ class QuantKVCache:
                                  f"{(self.batch, heads, tokens)} on {self.device}")
             lse_ptr = lse.data_ptr()
         ws, nbytes = self._work(("attend", heads, tokens, bool(add_weight)),
-                                lambda: B.sa_kv4_attend_bytes(self._c, heads, tokens, add_weight))
+                                lambda: B.sa_kv4_attend_bytes(self._c, heads, tokens, add_weight),
+                                stream)
         B.sa_kv4_attend(self._c, q, o, _DTYPES[Q.dtype], heads, tokens, self._counts(counts),
                         causal, scale, lse_ptr, add_weight, ws, nbytes, self._stream(stream))
         return out
@@ -180,7 +187,7 @@ class QuantKVCache:
     def evict(self, keep, first=0, recent=0, stream=None):
         """Evict every sequence down to ``keep`` rows per KV head: the first ``first`` and the
         last ``recent`` rows appended stay, of the others those of the largest weight."""
-        ws, nbytes = self._work("evict", lambda: B.sa_kv4_evict_bytes(self._c))
+        ws, nbytes = self._work("evict", lambda: B.sa_kv4_evict_bytes(self._c), stream)
         B.sa_kv4_evict(self._c, keep, first, recent, ws, nbytes, self._stream(stream))
 
     def rows_held(self):

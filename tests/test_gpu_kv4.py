@@ -686,6 +686,24 @@ def test_calls_on_another_stream():
     assert p.gpu.seq[0].tolist() == [20]
 
 
+def test_memory_comes_from_the_stream_that_writes_it():
+    c = sa.QuantKVCache(1, 2, 64, 256)
+    side = torch.cuda.Stream()
+    K = normal("sm", (1, 50, 2, 64), BF).cuda()
+    torch.cuda.synchronize()
+    c.append(K, K, stream=side)
+    out = c.attend(K, stream=side, add_weight=True)
+    here = c.attend(K)
+    assert c.check(side) == sa.SA_OK
+    at = {t.data_ptr(): s["stream"] for t in (out, here, c._workspaces[-1])
+          for s in torch.cuda.memory_snapshot()
+          if s["address"] <= t.data_ptr() < s["address"] + s["total_size"]}
+    assert at == {out.data_ptr(): side.cuda_stream, c._workspaces[-1].data_ptr(): side.cuda_stream,
+                  here.data_ptr(): torch.cuda.current_stream().cuda_stream}
+    torch.cuda.synchronize()
+    assert torch.equal(out, here)
+
+
 @pytest.mark.parametrize("T", [1, 12, 200])
 def test_lengths_are_those_behind_a_long_append(T):
     """Kernels may begin while the ones in front of them run: a sequence of calls without a

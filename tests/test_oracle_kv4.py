@@ -113,3 +113,8 @@ def test_null_and_host_buffers_are_refused():
         sa.sa_kv4_reset(bad)
     assert "16-byte aligned" in sa.last_error()
     assert ctypes.sizeof(sa.SaKv4Cache) == 16 + 8 * 8 and ctypes.sizeof(sa.SaRows) == 32
+
+
+def test_a_cache_off_the_gpu_is_refused():
+    with pytest.raises(ValueError, match="must be on a GPU"):
+        sa.QuantKVCache(1, 2, 64, 128, device="cpu")
