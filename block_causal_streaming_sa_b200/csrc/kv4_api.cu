@@ -26,6 +26,9 @@ using sa::NvtxRange;
 namespace {
 
 constexpr int kMaxGridYZ = 65535;
+// Rows of a sequence: a pass of one block of queries over as many stays within the
+// kernels' bounded waits (a second), and all row counts within 32 bits.
+constexpr int kMaxCapacity = 1 << 26;
 
 int refuse(int code, const std::string& why) {
   g_error = "kv4: " + why;
@@ -62,7 +65,7 @@ int check_sizes(const sa_kv4_cache* c) {
   if (c->capacity % 128 != 0)
     return refuse(SA_ERR_INVALID_ARG, "capacity must be a multiple of 128");
   if (c->batch > kMaxGridYZ || c->kv_heads > kMaxGridYZ ||
-      1LL * c->batch * c->kv_heads > (1LL << 24) || c->capacity > (1 << 30))
+      1LL * c->batch * c->kv_heads > (1LL << 24) || c->capacity > kMaxCapacity)
     return refuse(SA_ERR_UNSUPPORTED, "too many sequences, heads or rows");
   return SA_OK;
 }

@@ -452,7 +452,8 @@ typedef struct {
   int32_t batch;      /* B >= 1 sequences */
   int32_t kv_heads;   /* Hk >= 1 */
   int32_t head_dim;   /* D: 64 or 128 */
-  int32_t capacity;   /* N: rows each sequence can hold, a multiple of 128 */
+  int32_t capacity;   /* N: rows each sequence can hold, a multiple of 128, at most
+                         2^26 */
   uint8_t* k_codes;   /* [B, Hk, N, D / 2] */
   uint8_t* v_codes;   /* [B, Hk, N, D / 2] */
   uint8_t* k_scales;  /* [B, Hk, N, D / 16] */

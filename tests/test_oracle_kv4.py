@@ -118,3 +118,14 @@ def test_null_and_host_buffers_are_refused():
 def test_a_cache_off_the_gpu_is_refused():
     with pytest.raises(ValueError, match="must be on a GPU"):
         sa.QuantKVCache(1, 2, 64, 128, device="cpu")
+
+
+def test_sizes_at_the_limits():
+    assert sa.sa_kv4_evict_bytes(_cache(capacity=1 << 26)) == 2 * (4 << 26)
+    assert sa.sa_kv4_attend_bytes(_cache(capacity=1 << 26), 2, 1, True) > 2 * (8 << 26)
+    for bad in (dict(capacity=(1 << 26) + 128), dict(kv_heads=1 << 16),
+                dict(batch=1 << 15, kv_heads=1 << 10)):
+        assert sa.sa_kv4_evict_bytes(_cache(**bad)) == 0, bad
+        assert "too many" in sa.last_error()
+    assert sa.sa_kv4_attend_bytes(_cache(), 2, (1 << 24) + 1) == 0
+    assert sa.sa_kv4_attend_bytes(_cache(kv_heads=1), 65535, 1 << 20) == 0
