@@ -631,22 +631,22 @@ __global__ void __launch_bounds__(128, DecodeShape<D, NT>::kBlocksPerSm)
 
 // Merge of the partial results of kv4_decode_kernel, W warps per query row, and, where
 // that left the scores (up to 8 query rows), the rows' weights. Blocks below
-// join_blocks merge; the others add weights, kJoinKeys cache rows of one (sequence, KV
-// head) each: they derive the log-sum-exp of its query rows from the same partial
+// join_blocks merge; the others add weights, a range of rows of one (sequence, KV
+// head) each, kJoinKeys at a time: they derive the log-sum-exp of its query rows from the same partial
 // results, so no order among blocks is needed.
 constexpr int kJoinKeys = 512;
 
 template <int D, int kRows, int W, int kDtype>
 __global__ void __launch_bounds__(128)
-    kv4_join_kernel(const __grid_constant__ Kv4AttendParams p, int blocks, int join_blocks) {
+    kv4_join_kernel(const __grid_constant__ Kv4AttendParams p, int blocks, int join_blocks,
+                    int parts) {
   const Kv4& c = p.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool joins = static_cast<int>(blockIdx.x) < join_blocks;
   // join: block = (unit, 4 / W rows of it); weights (8 query rows or fewer): block =
-  // (head plane, chunk of cache rows)
+  // (head plane, one of `parts` ranges of its rows)
   constexpr int kGroups = kRows * W / 4;
-  const int chunks = (c.N + kJoinKeys - 1) / kJoinKeys;
-  const int id = joins ? blockIdx.x / kGroups : (blockIdx.x - join_blocks) / chunks;
+  const int id = joins ? blockIdx.x / kGroups : (blockIdx.x - join_blocks) / parts;
   const int units_b = c.H * p.row_blocks;
   const int b = joins ? id / units_b : id / c.H;
   // The lengths were there before the decode kernel let this one begin: the schedule
@@ -654,12 +654,19 @@ __global__ void __launch_bounds__(128)
   __threadfence();
   const int held = rows_held(c, b), n_tok = tokens_of(p.counts, b, p.T);
   const int n_rows = n_tok * p.group;
-  const Line line = line_of(p, blocks, 32, lane);
-  const int b0 = tiles_before(p, b, 32, lane);
-  const int per_unit = unit_tiles(p, b, 32);
+  const int part_rows = ((held + parts - 1) / parts + 127) / 128 * 128;
+  const int j0 = joins ? 0 : static_cast<int>((blockIdx.x - join_blocks) % parts) * part_rows;
+  const bool idle = n_rows == 0 || (!joins && j0 >= held);
+  Line line = {1, 0};
+  int b0 = 0, per_unit = 0;
+  if (!idle) {
+    line = line_of(p, blocks, 32, lane);
+    b0 = tiles_before(p, b, 32, lane);
+    per_unit = unit_tiles(p, b, 32);
+  }
   begin_early();
   wait_for_previous();
-  if (n_rows == 0) return;
+  if (idle) return;
 
   // Partial results of one query row: `n` slots from `first` on.
   auto slots_of = [&](int unit_in_b, size_t& first, int& n) {
@@ -774,12 +781,43 @@ __global__ void __launch_bounds__(128)
     return;
   }
 
-  // ---- weights of rows j0 .. of KV head h
+  // ---- weights of rows j0 .. of KV head h. Scores and weights are asked for first: the
+  // log-sum-exps are a chain of dependent loads of their own (ragged batch of 16, 8
+  // heads, 1.4 M rows in all: 69 us against 71; long ranges, few blocks: 66).
   const int h = id % c.H;
-  const int j0 = static_cast<int>((blockIdx.x - join_blocks) % chunks) * kJoinKeys;
-  if (j0 >= held) return;
-  extern __shared__ float s_lse[];  // [score_rows]
-  for (int row = warp; row < p.score_rows; row += 4) {
+  const size_t plane = (static_cast<size_t>(b) * c.H + h) * c.N;
+  constexpr int kKeys = kJoinKeys / 128;
+  const int j1 = min(j0 + part_rows, held);
+  float2 x[kKeys][4];
+  float w[kKeys];
+  auto load = [&](int from) {
+#pragma unroll
+    for (int k = 0; k < kKeys; ++k) {
+      const int j = from + k * 128 + threadIdx.x;
+      const float* src = p.scores + (plane + j) * p.score_rows;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) x[k][r] = make_float2(-INFINITY, -INFINITY);
+      if (j < j1) {
+        if ((p.score_rows & 3) == 0) {
+#pragma unroll
+          for (int r = 0; r < 4; r += 2)
+            if (2 * r < p.score_rows) {
+              const float4 v = reinterpret_cast<const float4*>(src)[r / 2];
+              x[k][r] = make_float2(v.x, v.y);
+              x[k][r + 1] = make_float2(v.z, v.w);
+            }
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (2 * r < p.score_rows) x[k][r] = reinterpret_cast<const float2*>(src)[r];
+        }
+      }
+      w[k] = j < j1 ? c.weight[plane + j] : 0.f;
+    }
+  };
+  load(j0);
+  __shared__ float2 s_lse[4];  // of 8 query rows
+  for (int row = warp; row < 8; row += 4) {
     float mx = -INFINITY, sum = 0.f;
     if (row < n_rows) {
       size_t first;
@@ -791,25 +829,33 @@ __global__ void __launch_bounds__(128)
       for (int k = 16; k; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, k));
       const float ref = mx == -INFINITY ? 0.f : mx;
       for (int s = lane; s < n; s += 32) {
-        const float2 x = ml[static_cast<size_t>(s) * kRows];
-        sum += x.y * ptx::ex2(x.x - ref);
+        const float2 v = ml[static_cast<size_t>(s) * kRows];
+        sum += v.y * ptx::ex2(v.x - ref);
       }
 #pragma unroll
       for (int k = 16; k; k >>= 1) sum += __shfl_xor_sync(~0u, sum, k);
     }
     // rows that are not there, or see nothing, add 0
-    if (lane == 0) s_lse[row] = row < n_rows && sum != 0.f ? mx + log2f(sum) : INFINITY;
+    if (lane == 0)
+      reinterpret_cast<float*>(s_lse)[row] =
+          row < n_rows && sum != 0.f ? mx + log2f(sum) : INFINITY;
   }
   __syncthreads();
-  const size_t plane = (static_cast<size_t>(b) * c.H + h) * c.N;
-  for (int j = j0 + threadIdx.x; j < min(j0 + kJoinKeys, held); j += 128) {
-    const float* src = p.scores + (plane + j) * p.score_rows;
-    float sum = 0.f;
-    for (int r = 0; r < p.score_rows; r += 2) {
-      const float2 x = *reinterpret_cast<const float2*>(src + r);
-      sum += ptx::ex2(x.x - s_lse[r]) + ptx::ex2(x.y - s_lse[r + 1]);
+#pragma unroll 1
+  for (int from = j0; from < j1; from += kJoinKeys) {
+    if (from > j0) load(from);
+#pragma unroll
+    for (int k = 0; k < kKeys; ++k) {
+      const int j = from + k * 128 + threadIdx.x;
+      float sum = 0.f;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float2 lse = s_lse[r];
+        if (2 * r < p.score_rows)
+          sum += ptx::ex2(x[k][r].x - lse.x) + ptx::ex2(x[k][r].y - lse.y);
+      }
+      if (j < j1) c.weight[plane + j] = w[k] + sum;
     }
-    c.weight[plane + j] += sum;
   }
 }
 

@@ -308,13 +308,17 @@ bool launch_decode(const sa::Kv4AttendParams& p, cudaStream_t s) {
   launch_after(sa::kv4_decode_kernel<D, NT, kDtype, kScores>, dim3(blocks), dim3(128), S::kSmem, s,
                p);
   const int units = p.c.B * p.c.H * p.row_blocks;
-  const int chunks = (p.c.N + sa::kJoinKeys - 1) / sa::kJoinKeys;
+  // weights: as many blocks as run at once (six an SM), twice, since lengths differ; of
+  // 512 rows or more
+  const int parts = std::max(std::min(2 * 6 * std::min(sm_count(), kMostSms) / (p.c.B * p.c.H),
+                                      (p.c.N + sa::kJoinKeys - 1) / sa::kJoinKeys),
+                             1);
   // Long rows leave many partial results: a block merges one query row's. With 8 or
   // fewer a warp a row is enough.
   auto join = [&](auto kernel, int warps) {
     const int merge = units * (S::kRows * warps / 4);
-    launch_after(kernel, dim3(merge + (kScores ? p.c.B * p.c.H * chunks : 0)), dim3(128),
-                 kScores ? p.score_rows * sizeof(float) : 0, s, p, blocks, merge);
+    launch_after(kernel, dim3(merge + (kScores ? p.c.B * p.c.H * parts : 0)), dim3(128), 0, s,
+                 p, blocks, merge, parts);
   };
   if (blocks > 8 * units)
     join(sa::kv4_join_kernel<D, S::kRows, 4, kDtype>, 4);
