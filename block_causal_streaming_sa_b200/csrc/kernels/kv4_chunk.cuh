@@ -310,20 +310,43 @@ __device__ __noinline__ void chunk_epilogue(const Kv4AttendParams& p, uint32_t t
   }
   const float inv = lsum == 0.f ? 0.f : 1.f / lsum;  // NaN stays NaN
   const int t = row / p.group, hq = h * p.group + row % p.group;
-  uint16_t* dst = static_cast<uint16_t*>(p.o.data) + b * p.o.sb + t * p.o.st + hq * p.o.sh;
+  // 32 columns at a time; four lanes exchange theirs, so that a store covers 64 bytes of
+  // 8 rows. With each lane storing its own row the 32 lines of an instruction took 4000
+  // of the epilogue's 6000 cycles.
+  const int lane = threadIdx.x & 31, piece = lane & 3;
+  const long long own = row < n_rows ? b * p.o.sb + t * p.o.st + hq * p.o.sh : -1;
+  long long off[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) off[k] = __shfl_sync(~0u, own, (lane & ~3) + k);
+  uint16_t* dst = static_cast<uint16_t*>(p.o.data) + piece * 8;
 #pragma unroll 1
   for (int j = 0; j < D / 32; ++j) {
     uint32_t o[32];
     ptx::tmem_ld32(tO + j * 32, o);
     ptx::tmem_wait_ld();
-    if (row < n_rows)
+    uint32_t v[4][4];  // this row's 16-byte pieces, then piece `piece` of the four rows
 #pragma unroll
-      for (int k = 0; k < 32; k += 8)
-        *reinterpret_cast<uint4*>(dst + j * 32 + k) = make_uint4(
-            pack2<kDtype>(__uint_as_float(o[k]) * inv, __uint_as_float(o[k + 1]) * inv),
-            pack2<kDtype>(__uint_as_float(o[k + 2]) * inv, __uint_as_float(o[k + 3]) * inv),
-            pack2<kDtype>(__uint_as_float(o[k + 4]) * inv, __uint_as_float(o[k + 5]) * inv),
-            pack2<kDtype>(__uint_as_float(o[k + 6]) * inv, __uint_as_float(o[k + 7]) * inv));
+    for (int k = 0; k < 16; ++k)
+      v[k >> 2][k & 3] = pack2<kDtype>(__uint_as_float(o[2 * k]) * inv,
+                                       __uint_as_float(o[2 * k + 1]) * inv);
+#pragma unroll
+    for (int bit = 1; bit < 4; bit <<= 1)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if ((k & bit) == 0)
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const bool upper = (lane & bit) != 0;
+            const uint32_t got =
+                __shfl_xor_sync(~0u, upper ? v[k][w] : v[k | bit][w], bit);
+            v[k][w] = upper ? got : v[k][w];
+            v[k | bit][w] = upper ? v[k | bit][w] : got;
+          }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (off[k] >= 0)
+        *reinterpret_cast<uint4*>(dst + off[k] + j * 32) =
+            make_uint4(v[k][0], v[k][1], v[k][2], v[k][3]);
   }
   if (row < n_rows) {
     const float lse2 = lsum == 0.f ? -INFINITY : m + log2f(lsum);
