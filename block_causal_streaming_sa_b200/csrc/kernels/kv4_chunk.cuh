@@ -250,36 +250,49 @@ __global__ void __launch_bounds__(256)
   const bool empty = item_tiles(p, held, n_tok, tile * 128 / kItemRows) == 0;
   const size_t tile_id = (static_cast<size_t>(b) * c.H + h) * p.q_tiles + tile;
   uint8_t* dst = p.q_img + tile_id * (128 * D * 2);
-  for (int i = threadIdx.x; i < 128 * C; i += 256) {
-    const int r = i / C, piece = i % C, row = tile * 128 + r;
-    const int t = row / p.group, hq = h * p.group + row % p.group;
-    uint4 w = make_uint4(0u, 0u, 0u, 0u);
-    if (row < n_rows)
-      w = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q.data) + b * p.q.sb +
-                                         t * p.q.st + hq * p.q.sh)[piece];
-    const float2 v[4] = {unpack2<kDtype>(w.x), unpack2<kDtype>(w.y), unpack2<kDtype>(w.z),
-                         unpack2<kDtype>(w.w)};
-    float amax = 0.f;
+  constexpr int kAhead = 4;  // loads under way a thread
+  static_assert(128 * C % (256 * kAhead) == 0);
+#pragma unroll 1
+  for (int i0 = threadIdx.x; i0 < 128 * C; i0 += 256 * kAhead) {
+    uint4 in[kAhead];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) amax = fmaxf(amax, fmaxf(fabsf(v[k].x), fabsf(v[k].y)));
+    for (int k = 0; k < kAhead; ++k) {
+      const int i = i0 + k * 256, row = tile * 128 + i / C;
+      const int t = row / p.group, hq = h * p.group + row % p.group;
+      in[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (row < n_rows)
+        in[k] = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q.data) +
+                                               b * p.q.sb + t * p.q.st + hq * p.q.sh)[i % C];
+    }
 #pragma unroll
-    for (int k = 1; k < C; k <<= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, k));
-    const float f = row_factor(amax);
-    uint32_t x[4];
+    for (int step = 0; step < kAhead; ++step) {
+      const int i = i0 + step * 256, r = i / C, piece = i % C, row = tile * 128 + r;
+      const int t = row / p.group, hq = h * p.group + row % p.group;
+      const uint4 w = in[step];
+      const float2 v[4] = {unpack2<kDtype>(w.x), unpack2<kDtype>(w.y), unpack2<kDtype>(w.z),
+                           unpack2<kDtype>(w.w)};
+      float amax = 0.f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) x[k] = pack2<SA_DTYPE_FP16>(v[k].x * f, v[k].y * f);
-    *reinterpret_cast<uint4*>(dst + tile_offset(r, piece)) = make_uint4(x[0], x[1], x[2], x[3]);
-    if (piece == 0)
-      p.row_scale[tile_id * 128 + r] = row < n_rows ? score_factor(p.scale_log2, f) : 0.f;
-    if (row >= n_rows) {
-      if (piece == 0) p.row_nlse[tile_id * 128 + r] = -INFINITY;  // such rows draw no weight
-    } else if (empty) {
-      uint16_t* o = static_cast<uint16_t*>(p.o.data) + b * p.o.sb + t * p.o.st + hq * p.o.sh;
-      *reinterpret_cast<uint4*>(o + piece * 8) = make_uint4(0u, 0u, 0u, 0u);
-      if (piece == 0) {
-        if (p.lse != nullptr)
-          p.lse[(static_cast<size_t>(b) * p.heads + hq) * p.T + t] = -INFINITY;
-        p.row_nlse[tile_id * 128 + r] = -INFINITY;
+      for (int k = 0; k < 4; ++k) amax = fmaxf(amax, fmaxf(fabsf(v[k].x), fabsf(v[k].y)));
+#pragma unroll
+      for (int k = 1; k < C; k <<= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, k));
+      const float f = row_factor(amax);
+      uint32_t x[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] = pack2<SA_DTYPE_FP16>(v[k].x * f, v[k].y * f);
+      *reinterpret_cast<uint4*>(dst + tile_offset(r, piece)) = make_uint4(x[0], x[1], x[2], x[3]);
+      if (piece == 0)
+        p.row_scale[tile_id * 128 + r] = row < n_rows ? score_factor(p.scale_log2, f) : 0.f;
+      if (row >= n_rows) {
+        if (piece == 0) p.row_nlse[tile_id * 128 + r] = -INFINITY;  // such rows draw no weight
+      } else if (empty) {
+        uint16_t* o = static_cast<uint16_t*>(p.o.data) + b * p.o.sb + t * p.o.st + hq * p.o.sh;
+        *reinterpret_cast<uint4*>(o + piece * 8) = make_uint4(0u, 0u, 0u, 0u);
+        if (piece == 0) {
+          if (p.lse != nullptr)
+            p.lse[(static_cast<size_t>(b) * p.heads + hq) * p.T + t] = -INFINITY;
+          p.row_nlse[tile_id * 128 + r] = -INFINITY;
+        }
       }
     }
   }
