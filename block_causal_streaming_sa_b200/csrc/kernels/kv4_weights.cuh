@@ -3,8 +3,10 @@
 // after the attention has left every query's log-sum-exp.
 //
 // One product and one exponential per (query row, cache row): 128 x 128 exponentials
-// take twice the cycles of their product, and a step moves about as many cycles' worth
-// of shared memory (operands 64 KB, the query tile 32, the rows' scales 32).
+// take twice the cycles of their product. A quarter of them goes to the FMA pipe, and
+// then the softmax warps' issue slots are the bound: more there is slower (3/8: 1.65 ms in
+// the measurement below), and halving the operands' shared memory traffic by pairs of SMs
+// gains nothing (1.58).
 // Transposed scores S^T = K Q^T put a cache row on a thread, so its sum stays in the
 // thread's registers over all queries: no reduction across threads and no atomics,
 // the same bits on every run. K is converted once per key tile; query tiles stream
@@ -17,7 +19,7 @@
 //    the four tensor memory buffers of the same numbers; three warpgroups take the steps
 //    in turn; one converts key tiles, one ahead.
 //
-// Measured: 10800 x 43200 rows, 12 heads, D 128: 1.56 ms.
+// Measured: 10800 x 43200 rows, 12 heads, D 128: 1.54 ms.
 #pragma once
 
 #include "kv4_chunk.cuh"
@@ -226,7 +228,7 @@ __global__ void __launch_bounds__(WeightShape<D>::kThreads, 1)
                        nl.w);
             e0 = ptx::ex2(e0);
             e1 = ptx::ex2(e1);
-            if (k % 8 == 4) {  // a quarter (1.61 ms at 720p; none 1.87, half 1.87)
+            if (k % 8 == 4) {  // a quarter, see above
               exp2_fma2(e2, e3, e2, e3);
             } else {
               e2 = ptx::ex2(e2);
