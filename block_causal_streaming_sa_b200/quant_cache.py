@@ -18,7 +18,8 @@ class QuantKVCache:
     Tensors are bf16 or fp16 [B, T, heads, D] on the cache's device, D contiguous, the other
     strides multiples of 8 (a slice of a fused projection will do). K and Q come with
     their position encoding applied. ``counts`` (int32 [B] on the device, or None for T each)
-    gives the valid tokens of each sequence of a padded batch.
+    gives the valid tokens of each sequence of a padded batch. For serving: no call records
+    gradients.
 
     The buffers are attributes: ``k_codes``, ``v_codes`` [B, Hk, N, D / 2] and
     ``k_scales``, ``v_scales`` [B, Hk, N, D / 16] (uint8), ``pos`` (int32) and ``weight``
