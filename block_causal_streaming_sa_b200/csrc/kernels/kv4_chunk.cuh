@@ -749,7 +749,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(512, 1)
                        fmaxf(ptx::fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]))) *
                  sl;
         };
-        // P = 2^(s * scale - m) of a half; returns the row's sum
+        // P = 2^(s * scale - m) of a half, m the reference (kRefBelow); returns the row's sum
         auto exponentials = [&](uint32_t to) {
           // a row can meet keys wholly behind its last one before any it sees
           const float nm = m == -INFINITY ? 0.f : -m;
@@ -773,12 +773,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(512, 1)
           }
           return ((rs[0] + rs[1]) + (rs[2] + rs[3])) + ((rs[4] + rs[5]) + (rs[6] + rs[7]));
         };
-        // Raises the maximum to m_new; returns what the sum and O so far scale with.
-        auto raise = [&](float m_new) {
+        // Raises the reference where the half's largest score mx asks for it; returns what
+        // the sum and O so far scale with.
+        auto raise = [&](float mx) {
           float alpha = 1.f;
-          if (m_new > m + 8.0f) {
-            alpha = ptx::ex2(m - m_new);
-            m = m_new;
+          if (mx > m + kRefTop) {
+            alpha = ptx::ex2(m - (mx - kRefBelow));
+            m = mx - kRefBelow;
           }
           lsum *= alpha;
           if (t > walk.t0) chunk_scale_columns<D>(tO, alpha);  // the first P V overwrites O
@@ -796,12 +797,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(512, 1)
         float rs = 0.f;
         if (used) {
           const float mx = row_max();
-          if (__any_sync(~0u, mx > m + 8.0f)) {
+          if (__any_sync(~0u, mx > m + kRefTop)) {
             // half b is issued behind the last P V: with it O stands still
             wait_b();
             if (!ok) break;
             ptx::tc_fence_after();
-            raise(fmaxf(m, mx));
+            raise(mx);
           }
           rs = exponentials(tA);
         }
@@ -813,11 +814,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(512, 1)
         if (lane == 0) arrive_leader(read);
         if (used) {
           const float mx = row_max();
-          if (__any_sync(~0u, mx > m + 8.0f)) {
+          if (__any_sync(~0u, mx > m + kRefTop)) {
             // half a's P is scaled too (its second rounding to fp16, in the few tiles where
             // a maximum grows that much)
             ptx::tmem_wait_st();
-            const float alpha = raise(fmaxf(m, mx));
+            const float alpha = raise(mx);
             rs *= alpha;
             chunk_scale_p(tA, alpha);
           }

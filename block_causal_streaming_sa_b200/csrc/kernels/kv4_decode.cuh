@@ -16,9 +16,9 @@
 //    the conversion, which then yields pairs of rows. P^T comes from S^T by
 //    transposing 8 x 8 blocks (movmatrix); both keep query rows on the same lanes, so
 //    the softmax statistics never move.
-//  * The running maximum of a query row is raised only when a score exceeds it by
-//    more than 2^8 (checked by one vote a tile): no reduction across lanes otherwise.
-//    P stays below 2^8 and l and O are fp32.
+//  * The reference of a query row (kRefBelow) is raised only when a score exceeds it by
+//    more than kRefTop (checked by one vote a tile): no reduction across lanes otherwise.
+//    l and O are fp32.
 //  * Each warp streams tiles of 32 rows through a ring of its own (a bulk copy by
 //    each of four lanes, an mbarrier a stage), so warps never wait for one another.
 //  * The rows of all sequences and heads are one line of tiles, cut into equal
@@ -36,8 +36,8 @@
 
 namespace sa {
 
-// The running maximum before any score: finite, so that a masked score (-inf) minus it
-// is -inf, and below every score.
+// The reference before any score: finite, so that a masked score (-inf) minus it is -inf,
+// and below every score.
 constexpr float kNoScore = -3.402823466e38f;
 
 template <int D, int NT>
@@ -472,7 +472,7 @@ __global__ void __launch_bounds__(128, DecodeShape<D, NT>::kBlocksPerSm)
             }
         return top;
       };
-      if (__any_sync(~0u, subtract() > 8.f)) {
+      if (__any_sync(~0u, subtract() > kRefTop)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -481,7 +481,7 @@ __global__ void __launch_bounds__(128, DecodeShape<D, NT>::kBlocksPerSm)
                              fmaxf(s[1][nt][i], s[1][nt][i + 2]));
 #pragma unroll
             for (int k = 4; k < 32; k <<= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, k));
-            mx = fmaxf(mx * sl[nt][i], m[nt][i]);
+            mx = fmaxf(mx * sl[nt][i] - kRefBelow, m[nt][i]);
             const float a = mx > m[nt][i] ? ptx::ex2(m[nt][i] - mx) : 1.f;
             m[nt][i] = mx;
             l[nt][i] *= a;

@@ -32,6 +32,17 @@ __device__ __forceinline__ void exp2_fma2(float& y0, float& y1, float x0, float 
   y1 = __int_as_float(__float_as_int(q1) + (__float_as_int(t1) << 23));
 }
 
+// P = 2^(score - reference) enters the second product as fp16. The reference follows the
+// running maximum from kRefBelow below it, and is raised once a score exceeds it by more
+// than kRefTop: P stays below 2^15 (fp16 reaches 2^16), and what is kRefBelow + 14 powers of
+// two below the maximum still has all eleven bits, what is kRefBelow + 25 below it some.
+// Behind a row that dominates (the first of a sequence often does) everything else lies
+// far below the maximum, and its roundings add up over a long cache instead of cancelling:
+// with the reference at the maximum, whatever lay 17 nats below it lost its share of O. Five
+// powers of two between the two bounds keep the raises rare: 8, 5, 4, 3 of them take 788, 784,
+// 798, 849 us (6120 x 24480 rows, 12 heads, scores of a deviation of 1.1 nats).
+constexpr float kRefBelow = 10.0f, kRefTop = 15.0f;
+
 // What a staged row's scores are multiplied with. Kept above zero: a masked score is
 // -inf, and 0 * -inf is not.
 __device__ __forceinline__ float score_factor(const float scale_log2, float row_factor) {
@@ -64,7 +75,7 @@ struct Kv4AttendParams {
   // few query rows (kv4_decode.cuh)
   int row_blocks;  // blocks of query rows per (sequence, KV head)
   float* part_o;   // [slot][rows of a block][D], not normalised
-  float2* part_ml; // [slot][rows of a block]: maximum (base 2), sum
+  float2* part_ml; // [slot][rows of a block]: reference (base 2), sum
   float* scores;   // [B][H][N][score_rows], base 2
   int score_rows;
   // many query rows (kv4_chunk.cuh, kv4_weights.cuh)

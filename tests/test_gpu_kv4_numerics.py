@@ -1,0 +1,50 @@
+"""Attention over the 4-bit cache where numbers are far apart, against the float64 oracle."""
+
+import numpy as np
+import pytest
+import torch
+
+import block_causal_streaming_sa_b200 as sa
+from oracle import kv4
+from test_gpu_kv4 import BF, HALF, HF, Pair, f64, normal, score_error
+
+pytestmark = pytest.mark.gpu
+
+# P enters the second product as fp16 with the row's largest at 2^10 or above (its half step
+# below 2^-14 is 2^-25): relative to the largest, what a rounding of a small P is off by.
+P_FLOOR = 2.0 ** -(25 + 10)
+
+
+@pytest.mark.parametrize("nats,n", [(12.0, 4093), (17.4, 43_200), (20.0, 262_144)])
+@pytest.mark.parametrize("T,D,dtype,causal", [(1, 128, BF, False), (8, 64, HF, True),
+                                              (24, 128, HF, False), (64, 64, BF, True),
+                                              (130, 128, BF, False), (300, 64, HF, True),
+                                              (513, 128, HF, True)])
+def test_attend_behind_a_row_that_dominates(T, D, dtype, causal, nats, n):
+    """The first row's score lies far above all others', which are nearly even, and its V is
+    zero: O is what the others have together, each far below the largest probability."""
+    p = Pair(1, 1, D, -(-n // 128) * 128, dtype)
+    tag = ("sink", T, D, nats)
+    K, V = normal((tag, "k"), (1, n, 1, D), dtype, 0.2), normal((tag, "v"), (1, n, 1, D), dtype, 0.2)
+    V += 0.5
+    K[..., 0] = 0
+    K[0, 0, 0], V[0, 0, 0] = 0, 0
+    K[0, 0, 0, 0] = nats * D ** 0.5 / 4
+    Q = normal((tag, "q"), (1, T, 1, D), dtype)
+    Q[..., 0] = 4
+    p.gpu.append(K.cuda(), V.cuda())
+    p.ref.append(f64(K), f64(V))
+    out = torch.empty((1, T, 1, D), dtype=dtype, device="cuda")
+    lse = torch.empty((1, 1, T), device="cuda")
+    p.gpu.attend(Q.cuda(), causal=causal, out=out, lse=lse, add_weight=True)
+    O, L, A, E = p.ref.attend(f64(Q), causal=causal, add_weight=True)
+    err = score_error(D, E)
+    # as for any attention (p off by e^err, its rounding by half a step, the normalisation, the
+    # output's rounding), and small p by P_FLOOR of the largest
+    tol = (2 * np.transpose(err, (0, 2, 1))[..., None] + 2.0 ** -11 + 2.0 ** -20) * A \
+        + P_FLOOR * np.abs(p.ref.v[0][0]).sum(axis=0) + HALF[dtype] * np.abs(O) + 1e-8
+    d = np.abs(f64(out) - O)
+    assert np.all(d <= tol), f"off by {(d / np.abs(O)).max():.2e} of O, {(d / tol).max():.2f} of the tolerance"
+    assert np.all(np.abs(f64(lse) - L) <= err + 4 * 2.0 ** -24 * np.abs(L))
+    p.check_weights(1, float(E.max()))
+    assert p.gpu.check() == sa.SA_OK
