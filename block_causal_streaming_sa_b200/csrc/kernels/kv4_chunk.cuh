@@ -834,7 +834,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(512, 1)
       if (!__all_sync(~0u, wait(S::OFINAL(i), items & 1))) break;
       ++items;
       ptx::tc_fence_after();
-      if (m == -INFINITY) lsum = 0.f;  // no key seen: what the polynomial left of 2^-inf
       if (used)
         chunk_epilogue<D, kDtype>(p, tO, m, lsum, walk.t0 == 0 && walk.t1 == walk.n,
                                   partial_slot(pair, walk.t0), walk.b, walk.h, row, n_rows);

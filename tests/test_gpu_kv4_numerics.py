@@ -48,3 +48,22 @@ def test_attend_behind_a_row_that_dominates(T, D, dtype, causal, nats, n):
     assert np.all(np.abs(f64(lse) - L) <= err + 4 * 2.0 ** -24 * np.abs(L))
     p.check_weights(1, float(E.max()))
     assert p.gpu.check() == sa.SA_OK
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("T,n", [(1, 200), (20, 200), (130, 200), (130, 30_000)])
+def test_a_query_that_is_not_finite_has_a_nan_lse(T, n, value):
+    """Few and many query rows, whole items and items split over blocks; -inf is for queries
+    that see no row, and the other queries' lse stay."""
+    p = sa.QuantKVCache(1, 1, 128, -(-n // 128) * 128)
+    K = normal(("nlse", n), (1, n, 1, 128), BF).cuda()
+    p.append(K, K)
+    Q = normal(("nlse", T), (1, T, 2, 128), BF).cuda()
+    want, lse = (torch.empty((1, 2, T), device="cuda") for _ in range(2))
+    p.attend(Q, lse=want)
+    Q[0, 0, 1, 7] = value
+    out = p.attend(Q, lse=lse)
+    assert torch.isnan(lse[0, 1, 0]) and torch.isnan(out[0, 0, 1].float()).all()
+    same = torch.ones((1, 2, T), dtype=torch.bool, device="cuda")
+    same[0, 1, 0] = False
+    assert torch.equal(lse[same], want[same]) and torch.isfinite(want).all()
