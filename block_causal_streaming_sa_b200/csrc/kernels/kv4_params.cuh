@@ -9,16 +9,17 @@ namespace sa {
 // 2^x of two values on the FMA and integer pipes, for a share of the exponentials that
 // the exponential unit alone would hold up: x = n + f, n = round(x), 2^f on [-1/2, 1/2]
 // by a degree-5 polynomial (minimax in relative error, 2.4e-7 evaluated in fp32;
-// fit_exp2_poly.py), n added to the exponent. Below -127 the result is zero but for
-// the last bits of a subnormal. Softmax statistics come from these values, hence a
-// polynomial as exact as the unit (2^-22).
+// fit_exp2_poly.py), n added to the exponent. From -127 down the result is a subnormal's last
+// bit, for the caller to flush. Sums that rank rows come from these values, hence a
+// polynomial as exact as the unit (2^-22). A NaN comes out as if it were -127: an exponent
+// added to a NaN would leave a finite number as well.
 __device__ __forceinline__ void exp2_fma2(float& y0, float& y1, float x0, float x1) {
   constexpr float kRound = 12582912.0f;  // 1.5 * 2^23
   constexpr float c0 = 1.0000001192092896f, c1 = 0.6931469440460205f, c2 = 0.24022120237350464f;
   constexpr float c3 = 0.05550713092088699f, c4 = 0.009675540961325169f;
   constexpr float c5 = 0.0013276472454890609f;
-  asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x0));  // -127; a NaN stays one
-  asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x1));
+  x0 = fmaxf(x0, -127.0f);
+  x1 = fmaxf(x1, -127.0f);
   float t0, t1, f0, f1, q0, q1;
   ptx::fadd2(t0, t1, x0, x1, kRound, kRound);
   ptx::fadd2(f0, f1, t0, t1, -kRound, -kRound);  // n

@@ -26,6 +26,16 @@
 
 namespace sa {
 
+// Packed sums that take subnormals as zero: exponentials below 2^-126 add nothing, whichever
+// way they are taken.
+__device__ __forceinline__ void fadd2_ftz(float& d0, float& d1, float x0, float x1) {
+  asm("{\n\t.reg .b64 ra, rb;\n\t"
+      "mov.b64 ra, {%0, %1};\n\tmov.b64 rb, {%2, %3};\n\t"
+      "add.rn.ftz.f32x2 ra, ra, rb;\n\tmov.b64 {%0, %1}, ra;\n\t}"
+      : "+f"(d0), "+f"(d1)
+      : "f"(x0), "f"(x1));
+}
+
 template <int D>
 struct WeightShape {
   static constexpr int kTile = 128 * D * 2;
@@ -242,9 +252,17 @@ __global__ void __launch_bounds__(WeightShape<D>::kThreads, 1)
               e3 = col + 3 < hidden ? 0.f : e3;
             }
             const int a = (k & 4);
-            ptx::fadd2(acc[a], acc[a + 1], acc[a], acc[a + 1], e0, e1);
-            ptx::fadd2(acc[a + 2], acc[a + 3], acc[a + 2], acc[a + 3], e2, e3);
+            fadd2_ftz(acc[a], acc[a + 1], e0, e1);
+            fadd2_ftz(acc[a + 2], acc[a + 3], e2, e3);
           }
+        }
+        // A query whose log-sum-exp is NaN gives NaN to every row it sees; the polynomial
+        // dropped it. One vote over the tile's 128, each looked at only if it hits.
+        const float4 nl = *reinterpret_cast<const float4*>(scale + 128 + lane * 4);
+        if (__any_sync(~0u, isnan((nl.x + nl.y) + (nl.z + nl.w)))) {
+#pragma unroll 1
+          for (int col = max(hidden, 0); col < 128; ++col)
+            if (isnan(scale[128 + col])) acc[0] += scale[128 + col];
         }
         ptx::tc_fence_before();
         __syncwarp();

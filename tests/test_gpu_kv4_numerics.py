@@ -67,3 +67,49 @@ def test_a_query_that_is_not_finite_has_a_nan_lse(T, n, value):
     same = torch.ones((1, 2, T), dtype=torch.bool, device="cuda")
     same[0, 1, 0] = False
     assert torch.equal(lse[same], want[same]) and torch.isfinite(want).all()
+
+
+@pytest.mark.parametrize("T,causal", [(8, False), (24, False), (24, True), (130, False),
+                                      (130, True)])
+def test_a_nan_query_leaves_nan_weights_that_an_eviction_drops_first(T, causal):
+    """Whichever of eight neighbouring queries it is: the rows it sees draw NaN, the others
+    what they draw without it, bit for bit; NaN ranks below every number."""
+    D, n = 64, 200
+    p = Pair(1, 1, D, 256)
+    p.append(("nanw", T), n)
+    Q = normal(("nanw", T), (1, T, 1, D), BF).cuda()
+    p.gpu.weight.zero_()
+    p.gpu.attend(Q, causal=causal, add_weight=True)
+    want = p.gpu.weight[0, 0, :n].clone()
+    assert torch.isfinite(want).all() and (want > 0).all()
+    for t in range(T - 8, T):
+        q = Q.clone()
+        q[0, t, 0, 3] = float("nan")
+        p.gpu.weight.zero_()
+        p.gpu.attend(q, causal=causal, add_weight=True)
+        seen = n - T + t + 1 if causal else n
+        w = p.gpu.weight[0, 0, :n]
+        assert torch.isnan(w[:seen]).all(), t
+        assert torch.equal(w[seen:], want[seen:]), t
+    if causal:  # the last query sees every row: take the first of the eight
+        q = Q.clone()
+        q[0, T - 8] = float("nan")
+        p.gpu.weight.zero_()
+        p.gpu.attend(q, causal=True, add_weight=True)
+        p.gpu.evict(7)
+        assert p.gpu.pos[0, 0, :7].tolist() == list(range(n - 7, n))
+
+
+def test_rows_that_draw_nothing_from_many_queries_weigh_exactly_zero():
+    """Probabilities too small for fp32 add zero, whichever way their exponential is taken,
+    and so do the rows that pad the last tile of queries."""
+    D, n, T = 128, 300, 131
+    p = Pair(1, 1, D, 384)
+    K = torch.zeros((1, n, 1, D), dtype=BF)
+    K[0, 1:, 0, 0] = -60.0  # scores of 0, and of -4 * 60 * 11.3 = -2715 behind row 0
+    p.gpu.append(K.cuda(), K.cuda())
+    Q = torch.zeros((1, T, 1, D), dtype=BF)
+    Q[..., 0] = 4
+    p.gpu.attend(Q.cuda(), scale=11.3, add_weight=True)
+    assert (p.gpu.weight[0, 0, 1:n] == 0).all()
+    assert abs(float(p.gpu.weight[0, 0, 0]) - T) <= T * 2.0 ** -21
