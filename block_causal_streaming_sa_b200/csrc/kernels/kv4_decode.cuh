@@ -816,7 +816,8 @@ __global__ void __launch_bounds__(128)
     }
   };
   load(j0);
-  __shared__ float2 s_lse[4];  // of 8 query rows
+  __shared__ float2 s_lse[4];  // of 8 query rows, and the rows each sees
+  __shared__ int2 s_end[4];
   for (int row = warp; row < 8; row += 4) {
     float mx = -INFINITY, sum = 0.f;
     if (row < n_rows) {
@@ -835,10 +836,11 @@ __global__ void __launch_bounds__(128)
 #pragma unroll
       for (int k = 16; k; k >>= 1) sum += __shfl_xor_sync(~0u, sum, k);
     }
-    // rows that are not there, or see nothing, add 0
-    if (lane == 0)
-      reinterpret_cast<float*>(s_lse)[row] =
-          row < n_rows && sum != 0.f ? mx + log2f(sum) : INFINITY;
+    if (lane == 0) {
+      reinterpret_cast<float*>(s_lse)[row] = sum != 0.f ? mx + log2f(sum) : INFINITY;
+      reinterpret_cast<int*>(s_end)[row] =
+          row < n_rows ? rows_seen(p, held, n_tok, row / p.group) : 0;
+    }
   }
   __syncthreads();
 #pragma unroll 1
@@ -851,8 +853,11 @@ __global__ void __launch_bounds__(128)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const float2 lse = s_lse[r];
+        const int2 end = s_end[r];
+        // (by its place, not by its score of -inf: the lse may be NaN)
         if (2 * r < p.score_rows)
-          sum += ptx::ex2(x[k][r].x - lse.x) + ptx::ex2(x[k][r].y - lse.y);
+          sum += (j < end.x ? ptx::ex2(x[k][r].x - lse.x) : 0.f) +
+                 (j < end.y ? ptx::ex2(x[k][r].y - lse.y) : 0.f);
       }
       if (j < j1) c.weight[plane + j] = w[k] + sum;
     }

@@ -69,8 +69,8 @@ def test_a_query_that_is_not_finite_has_a_nan_lse(T, n, value):
     assert torch.equal(lse[same], want[same]) and torch.isfinite(want).all()
 
 
-@pytest.mark.parametrize("T,causal", [(8, False), (24, False), (24, True), (130, False),
-                                      (130, True)])
+@pytest.mark.parametrize("T,causal", [(8, False), (8, True), (24, False), (24, True),
+                                      (130, False), (130, True)])
 def test_a_nan_query_leaves_nan_weights_that_an_eviction_drops_first(T, causal):
     """Whichever of eight neighbouring queries it is: the rows it sees draw NaN, the others
     what they draw without it, bit for bit; NaN ranks below every number."""
@@ -98,6 +98,23 @@ def test_a_nan_query_leaves_nan_weights_that_an_eviction_drops_first(T, causal):
         p.gpu.attend(q, causal=True, add_weight=True)
         p.gpu.evict(7)
         assert p.gpu.pos[0, 0, :7].tolist() == list(range(n - 7, n))
+
+
+@pytest.mark.parametrize("T", [1, 20, 130])
+def test_a_query_whose_scores_are_all_minus_infinity_draws_nothing(T):
+    p = sa.QuantKVCache(1, 1, 64, 128)
+    K = torch.zeros((1, 90, 1, 64), dtype=BF, device="cuda")
+    K[..., 5] = -6
+    p.append(K, K)
+    Q = normal(("minus", T), (1, T, 1, 64), BF).cuda()
+    Q[0, 0, 0] = 0
+    Q[0, 0, 0, 5] = float("inf")  # the keys are 0 elsewhere: no score is NaN
+    lse = torch.empty((1, 1, T), device="cuda")
+    out = p.attend(Q, lse=lse, add_weight=True)
+    assert (out[0, 0] == 0).all() and lse[0, 0, 0] == -float("inf")
+    w = p.weight[0, 0, :90].double()
+    # the other queries see equal scores: their weight is T - 1 in all, spread evenly
+    assert torch.allclose(w, torch.full_like(w, (T - 1) / 90), rtol=1e-5)
 
 
 def test_rows_that_draw_nothing_from_many_queries_weigh_exactly_zero():
