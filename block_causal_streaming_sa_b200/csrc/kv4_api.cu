@@ -499,7 +499,7 @@ SA_API int sa_kv4_attend(const sa_kv4_cache* c, const sa_rows* Q, const sa_rows*
   const int D = c->head_dim;
   if (int rc = check_rows(Q, "Q", p.c.B, T, heads, D, false, device, &p.q); rc != SA_OK) return rc;
   if (int rc = check_rows(O, "O", p.c.B, T, heads, D, true, device, &p.o); rc != SA_OK) return rc;
-  if (O->data == Q->data) return refuse(SA_ERR_INVALID_ARG, "O must not alias Q");
+  if (T > 0 && O->data == Q->data) return refuse(SA_ERR_INVALID_ARG, "O must not alias Q");
   if (!std::isfinite(scale)) return refuse(SA_ERR_INVALID_ARG, "scale must be finite");
   std::string why;
   if (reinterpret_cast<uintptr_t>(lse) & 3u)

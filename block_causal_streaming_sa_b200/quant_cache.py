@@ -123,10 +123,13 @@ class QuantKVCache:
     def _work(self, key, nbytes, stream):
         """(pointer, bytes) of a workspace of at least `nbytes()`. One that became too small
         stays allocated: a captured graph, or a call under way on another stream, may use it.
-        Each is at least twice the one before, so all together are less than twice the last."""
+        Each is at least twice the one before, so all together are less than twice the last.
+        None for a call that needs none, or is refused for its sizes (the library says why)."""
         need = self._sizes.get(key)
         if need is None:
             need = self._sizes[key] = nbytes()
+        if need == 0:
+            return 0, 0
         have = self._workspaces[-1].numel() if self._workspaces else 0
         if have < need:
             if torch.cuda.is_current_stream_capturing():

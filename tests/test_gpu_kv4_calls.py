@@ -1,0 +1,34 @@
+"""Calls of the 4-bit cache that are rare but allowed, and refusals that must name their
+reason."""
+
+import pytest
+import torch
+
+import block_causal_streaming_sa_b200 as sa
+from test_gpu_kv4 import BF, Pair, normal
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("add_weight", [False, True])
+def test_attend_without_query_tokens_as_the_first_call(add_weight):
+    c = sa.QuantKVCache(2, 2, 64, 128)
+    none = torch.empty((2, 0, 4, 64), dtype=BF, device="cuda")
+    lse = torch.empty((2, 4, 0), device="cuda")
+    out = c.attend(none, lse=lse, add_weight=add_weight)
+    assert out.shape == none.shape and c._workspaces == []
+    some = normal("none", (2, 3, 2, 64), BF).cuda()
+    c.append(some, some)
+    weight = c.weight.clone()
+    c.attend(none, out=none, add_weight=add_weight, causal=True)
+    assert torch.equal(c.weight.view(torch.uint8), weight.view(torch.uint8))
+    assert c.check() == sa.SA_OK
+
+
+def test_unsupported_sizes_are_refused_by_the_library_whatever_came_before():
+    c = sa.QuantKVCache(1, 1, 96, 128)
+    q = torch.zeros((1, 1, 1, 96), dtype=BF, device="cuda")
+    for call in (lambda: c.attend(q), lambda: c.evict(5), lambda: c.append(q, q)):
+        with pytest.raises(sa.SaError, match="head_dim must be 64 or 128") as e:
+            call()
+        assert e.value.status == sa.SA_ERR_UNSUPPORTED
