@@ -132,7 +132,9 @@ class QuantKVCache:
             return 0, 0
         have = self._workspaces[-1].numel() if self._workspaces else 0
         if have < need:
-            if torch.cuda.is_current_stream_capturing():
+            with torch.cuda.device(self.device), torch.cuda.stream(stream):
+                capturing = torch.cuda.is_current_stream_capturing()
+            if capturing:
                 raise RuntimeError("make one call of this shape before capturing it: the "
                                    "workspace is too small")
             self._workspaces.append(self._empty(max(need, 2 * have), torch.uint8, stream))

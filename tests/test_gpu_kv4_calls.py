@@ -32,3 +32,27 @@ def test_unsupported_sizes_are_refused_by_the_library_whatever_came_before():
         with pytest.raises(sa.SaError, match="head_dim must be 64 or 128") as e:
             call()
         assert e.value.status == sa.SA_ERR_UNSUPPORTED
+
+
+def test_a_capture_on_the_stream_passed_in_needs_the_workspace_too():
+    """The call's stream captures, the current one does not."""
+    p = Pair(1, 1, 64, 128)
+    p.append("caps", 10)
+    q = normal("capsq", (1, 1, 1, 64), BF).cuda()
+    out = torch.empty_like(q)
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with pytest.raises(RuntimeError, match="before capturing"):
+        with torch.cuda.graph(graph, stream=side):
+            with torch.cuda.stream(other):
+                p.gpu.attend(q, out=out, stream=side)
+    torch.cuda.synchronize()
+    assert p.gpu._workspaces == []
+    want = p.gpu.attend(q)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        with torch.cuda.stream(other):
+            p.gpu.attend(q, out=out, stream=side)
+    graph.replay()
+    assert torch.equal(out, want)
