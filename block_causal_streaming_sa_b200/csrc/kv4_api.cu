@@ -161,7 +161,7 @@ int check_workspace(const void* ws, size_t bytes, size_t need, int device) {
 // Launch that may begin while the kernel before it on the stream drains; the kernel
 // itself waits until that one has finished (wait_for_previous, in every block).
 template <typename... P, typename... A>
-void launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
                   A... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
@@ -173,12 +173,14 @@ void launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cuda
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, kernel, args...);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-int launched(const char* what) {
-  const cudaError_t e = cudaGetLastError();
+// The result of a call from that of its launches. Kernels take what the ones before them
+// left in the workspace for granted, so the first launch that fails is a call's last.
+int launched(const char* what, cudaError_t e) {
   if (e == cudaSuccess) return SA_OK;
+  cudaGetLastError();
   return refuse(SA_ERR_CUDA, std::string(what) + " launch: " + cudaGetErrorString(e));
 }
 
@@ -301,12 +303,17 @@ AttendPlan plan_attend(const sa_kv4_cache* c, int heads, int T, bool weights) {
 }
 
 template <int D, int NT, int kDtype, bool kScores>
-bool launch_decode(const sa::Kv4AttendParams& p, cudaStream_t s) {
+cudaError_t launch_decode(const sa::Kv4AttendParams& p, cudaStream_t s) {
   using S = sa::DecodeShape<D, NT>;
-  if (!allow_smem<sa::kv4_decode_kernel<D, NT, kDtype, kScores>>(S::kSmem)) return false;
+  using W = sa::DecodeWeightShape<D>;
+  const bool second_pass = p.add_weight && !kScores;
+  if (!allow_smem<sa::kv4_decode_kernel<D, NT, kDtype, kScores>>(S::kSmem) ||
+      (second_pass && !allow_smem<sa::kv4_decode_weight_kernel<D, kDtype>>(W::kSmem)))
+    return cudaErrorInvalidConfiguration;
   const int blocks = std::min(sm_count(), kMostSms) * S::kBlocksPerSm;
-  launch_after(sa::kv4_decode_kernel<D, NT, kDtype, kScores>, dim3(blocks), dim3(128), S::kSmem, s,
-               p);
+  cudaError_t e = launch_after(sa::kv4_decode_kernel<D, NT, kDtype, kScores>, dim3(blocks),
+                               dim3(128), S::kSmem, s, p);
+  if (e != cudaSuccess) return e;
   const int units = p.c.B * p.c.H * p.row_blocks;
   // weights: as many blocks as run at once (six an SM), twice, since lengths differ; of
   // 512 rows or more
@@ -317,26 +324,21 @@ bool launch_decode(const sa::Kv4AttendParams& p, cudaStream_t s) {
   // fewer a warp a row is enough.
   auto join = [&](auto kernel, int warps) {
     const int merge = units * (S::kRows * warps / 4);
-    launch_after(kernel, dim3(merge + (kScores ? p.c.B * p.c.H * parts : 0)), dim3(128), 0, s,
-                 p, blocks, merge, parts);
+    return launch_after(kernel, dim3(merge + (kScores ? p.c.B * p.c.H * parts : 0)), dim3(128), 0,
+                        s, p, blocks, merge, parts);
   };
-  if (blocks > 8 * units)
-    join(sa::kv4_join_kernel<D, S::kRows, 4, kDtype>, 4);
-  else
-    join(sa::kv4_join_kernel<D, S::kRows, 1, kDtype>, 1);
-  if (p.add_weight && !kScores) {
-    using W = sa::DecodeWeightShape<D>;
-    if (!allow_smem<sa::kv4_decode_weight_kernel<D, kDtype>>(W::kSmem)) return false;
-    sa::Kv4AttendParams q = p;
-    q.row_blocks = 1;  // a unit has all query rows
-    launch_after(sa::kv4_decode_weight_kernel<D, kDtype>,
-                 dim3(std::min(sm_count(), kMostSms) * W::kBlocksPerSm), dim3(128), W::kSmem, s, q);
-  }
-  return true;
+  e = blocks > 8 * units ? join(sa::kv4_join_kernel<D, S::kRows, 4, kDtype>, 4)
+                         : join(sa::kv4_join_kernel<D, S::kRows, 1, kDtype>, 1);
+  if (e != cudaSuccess || !second_pass) return e;
+  sa::Kv4AttendParams q = p;
+  q.row_blocks = 1;  // a unit has all query rows
+  return launch_after(sa::kv4_decode_weight_kernel<D, kDtype>,
+                      dim3(std::min(sm_count(), kMostSms) * W::kBlocksPerSm), dim3(128), W::kSmem,
+                      s, q);
 }
 
 template <int D, int kDtype>
-bool launch_decode_nt(const sa::Kv4AttendParams& p, int nt, cudaStream_t s) {
+cudaError_t launch_decode_nt(const sa::Kv4AttendParams& p, int nt, cudaStream_t s) {
   if (nt == 1)
     return p.add_weight ? launch_decode<D, 1, kDtype, true>(p, s)
                         : launch_decode<D, 1, kDtype, false>(p, s);
@@ -346,25 +348,27 @@ bool launch_decode_nt(const sa::Kv4AttendParams& p, int nt, cudaStream_t s) {
 }
 
 template <int D, int kDtype>
-bool launch_chunk(const sa::Kv4AttendParams& p, cudaStream_t s) {
+cudaError_t launch_chunk(const sa::Kv4AttendParams& p, cudaStream_t s) {
   using S = sa::ChunkShape<D>;
-  if (!allow_smem<sa::kv4_chunk_kernel<D, kDtype>>(S::kSmem, 128)) return false;
-  const int blocks = std::min(sm_count(), kMostSms);
-  launch_after(sa::kv4_stage_kernel<D, kDtype>,
-               dim3(p.q_tiles + (p.add_weight ? 2 : 1), p.c.H, p.c.B), dim3(256), 0, s, p);
-  const int pairs = std::max(blocks / 2, 1);
-  launch_after(sa::kv4_chunk_kernel<D, kDtype>, dim3(2 * pairs), dim3(S::kThreads), S::kSmem, s,
-               p);
-  if (pairs > 1)
-    launch_after(sa::kv4_chunk_join_kernel<D, kDtype>, dim3(pairs - 1, sa::kItemRows / 32),
-                 dim3(128), 0, s, p, pairs);
-  if (!p.add_weight) return true;
   using W = sa::WeightShape<D>;
-  if (!allow_smem<sa::kv4_weight_kernel<D>>(W::kSmem)) return false;
-  launch_after(sa::kv4_weight_kernel<D>, dim3(blocks), dim3(W::kThreads), W::kSmem, s, p);
-  if (blocks > 1)
-    launch_after(sa::kv4_weight_join_kernel, dim3(blocks - 1), dim3(128), 0, s, p, blocks);
-  return true;
+  if (!allow_smem<sa::kv4_chunk_kernel<D, kDtype>>(S::kSmem, 128) ||
+      (p.add_weight && !allow_smem<sa::kv4_weight_kernel<D>>(W::kSmem)))
+    return cudaErrorInvalidConfiguration;
+  const int blocks = std::min(sm_count(), kMostSms), pairs = std::max(blocks / 2, 1);
+  cudaError_t e = launch_after(sa::kv4_stage_kernel<D, kDtype>,
+                               dim3(p.q_tiles + (p.add_weight ? 2 : 1), p.c.H, p.c.B), dim3(256),
+                               0, s, p);
+  if (e == cudaSuccess)
+    e = launch_after(sa::kv4_chunk_kernel<D, kDtype>, dim3(2 * pairs), dim3(S::kThreads), S::kSmem,
+                     s, p);
+  if (e == cudaSuccess && pairs > 1)
+    e = launch_after(sa::kv4_chunk_join_kernel<D, kDtype>, dim3(pairs - 1, sa::kItemRows / 32),
+                     dim3(128), 0, s, p, pairs);
+  if (e == cudaSuccess && p.add_weight)
+    e = launch_after(sa::kv4_weight_kernel<D>, dim3(blocks), dim3(W::kThreads), W::kSmem, s, p);
+  if (e == cudaSuccess && p.add_weight && blocks > 1)
+    e = launch_after(sa::kv4_weight_join_kernel, dim3(blocks - 1), dim3(128), 0, s, p, blocks);
+  return e;
 }
 
 size_t evict_bytes(const sa_kv4_cache* c) {
@@ -439,15 +443,12 @@ SA_API int sa_kv4_append(const sa_kv4_cache* c, const sa_rows* K, const sa_rows*
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const long long items = 1LL * T * (D / 16);
   const dim3 grid(static_cast<unsigned>(items > 0 ? (items + 255) / 256 : 1), p.c.H, p.c.B);
-  if (D == 128)
-    launch_after(dtype == SA_DTYPE_FP16 ? sa::kv4_append_kernel<128, SA_DTYPE_FP16>
-                                        : sa::kv4_append_kernel<128, SA_DTYPE_BF16>,
-                 grid, dim3(256), 0, s, p);
-  else
-    launch_after(dtype == SA_DTYPE_FP16 ? sa::kv4_append_kernel<64, SA_DTYPE_FP16>
-                                        : sa::kv4_append_kernel<64, SA_DTYPE_BF16>,
-                 grid, dim3(256), 0, s, p);
-  return launched("append");
+  const bool half = dtype == SA_DTYPE_FP16;
+  auto* kernel = D == 128 ? (half ? sa::kv4_append_kernel<128, SA_DTYPE_FP16>
+                                  : sa::kv4_append_kernel<128, SA_DTYPE_BF16>)
+                          : (half ? sa::kv4_append_kernel<64, SA_DTYPE_FP16>
+                                  : sa::kv4_append_kernel<64, SA_DTYPE_BF16>);
+  return launched("append", launch_after(kernel, grid, dim3(256), 0, s, p));
 }
 
 SA_API int sa_kv4_read(const sa_kv4_cache* c, int first, const sa_rows* K, const sa_rows* V,
@@ -469,15 +470,12 @@ SA_API int sa_kv4_read(const sa_kv4_cache* c, int first, const sa_rows* K, const
   DeviceGuard guard(device);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const dim3 grid(static_cast<unsigned>((1LL * T * (D / 16) + 255) / 256), p.c.H, p.c.B);
-  if (D == 128)
-    launch_after(dtype == SA_DTYPE_FP16 ? sa::kv4_read_kernel<128, SA_DTYPE_FP16>
-                                        : sa::kv4_read_kernel<128, SA_DTYPE_BF16>,
-                 grid, dim3(256), 0, s, p);
-  else
-    launch_after(dtype == SA_DTYPE_FP16 ? sa::kv4_read_kernel<64, SA_DTYPE_FP16>
-                                        : sa::kv4_read_kernel<64, SA_DTYPE_BF16>,
-                 grid, dim3(256), 0, s, p);
-  return launched("read");
+  const bool half = dtype == SA_DTYPE_FP16;
+  auto* kernel = D == 128 ? (half ? sa::kv4_read_kernel<128, SA_DTYPE_FP16>
+                                  : sa::kv4_read_kernel<128, SA_DTYPE_BF16>)
+                          : (half ? sa::kv4_read_kernel<64, SA_DTYPE_FP16>
+                                  : sa::kv4_read_kernel<64, SA_DTYPE_BF16>);
+  return launched("read", launch_after(kernel, grid, dim3(256), 0, s, p));
 }
 
 SA_API size_t sa_kv4_attend_bytes(const sa_kv4_cache* c, int heads, int T, int add_weight) {
@@ -526,16 +524,13 @@ SA_API int sa_kv4_attend(const sa_kv4_cache* c, const sa_rows* Q, const sa_rows*
   p.score_rows = plan.score_rows;
   DeviceGuard guard(device);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (plan.few) {
-    const bool ok = D == 128 ? (dtype == SA_DTYPE_FP16
-                                    ? launch_decode_nt<128, SA_DTYPE_FP16>(p, plan.nt, s)
-                                    : launch_decode_nt<128, SA_DTYPE_BF16>(p, plan.nt, s))
-                             : (dtype == SA_DTYPE_FP16
-                                    ? launch_decode_nt<64, SA_DTYPE_FP16>(p, plan.nt, s)
-                                    : launch_decode_nt<64, SA_DTYPE_BF16>(p, plan.nt, s));
-    if (!ok) return refuse(SA_ERR_CUDA, "shared memory of the attention kernel");
-    return launched("attention");
-  }
+  const bool half = dtype == SA_DTYPE_FP16;
+  if (plan.few)
+    return launched("attention",
+                    D == 128 ? (half ? launch_decode_nt<128, SA_DTYPE_FP16>(p, plan.nt, s)
+                                     : launch_decode_nt<128, SA_DTYPE_BF16>(p, plan.nt, s))
+                             : (half ? launch_decode_nt<64, SA_DTYPE_FP16>(p, plan.nt, s)
+                                     : launch_decode_nt<64, SA_DTYPE_BF16>(p, plan.nt, s)));
   p.q_tiles = plan.q_tiles;
   p.q_img = ws + plan.off_q;
   p.row_scale = reinterpret_cast<float*>(ws + plan.off_scale);
@@ -547,12 +542,10 @@ SA_API int sa_kv4_attend(const sa_kv4_cache* c, const sa_rows* Q, const sa_rows*
   };
   p.line = line(0, plan.items);
   p.weight_line = line(1, p.c.N / 128);
-  const bool ok = D == 128 ? (dtype == SA_DTYPE_FP16 ? launch_chunk<128, SA_DTYPE_FP16>(p, s)
-                                                     : launch_chunk<128, SA_DTYPE_BF16>(p, s))
-                           : (dtype == SA_DTYPE_FP16 ? launch_chunk<64, SA_DTYPE_FP16>(p, s)
-                                                     : launch_chunk<64, SA_DTYPE_BF16>(p, s));
-  if (!ok) return refuse(SA_ERR_CUDA, "resources of the attention kernel");
-  return launched("attention");
+  return launched("attention", D == 128 ? (half ? launch_chunk<128, SA_DTYPE_FP16>(p, s)
+                                                : launch_chunk<128, SA_DTYPE_BF16>(p, s))
+                                        : (half ? launch_chunk<64, SA_DTYPE_FP16>(p, s)
+                                                : launch_chunk<64, SA_DTYPE_BF16>(p, s)));
 }
 
 SA_API size_t sa_kv4_evict_bytes(const sa_kv4_cache* c) {
@@ -576,12 +569,8 @@ SA_API int sa_kv4_evict(const sa_kv4_cache* c, int keep, int first, int recent, 
   p.lists = static_cast<int32_t*>(workspace);
   DeviceGuard guard(device);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = c->head_dim == 128 ? launch_evict<128>(p, s) : launch_evict<64>(p, s);
-  if (e != cudaSuccess) {
-    cudaGetLastError();
-    return refuse(SA_ERR_CUDA, std::string("eviction launch: ") + cudaGetErrorString(e));
-  }
-  return SA_OK;
+  return launched("eviction",
+                  c->head_dim == 128 ? launch_evict<128>(p, s) : launch_evict<64>(p, s));
 }
 
 SA_API int sa_kv4_get_status(const sa_kv4_cache* c, sa_stream stream) {

@@ -1,6 +1,8 @@
 """Calls of the 4-bit cache that are rare but allowed, and refusals that must name their
 reason."""
 
+import ctypes
+
 import pytest
 import torch
 
@@ -56,3 +58,38 @@ def test_a_capture_on_the_stream_passed_in_needs_the_workspace_too():
             p.gpu.attend(q, out=out, stream=side)
     graph.replay()
     assert torch.equal(out, want)
+
+
+def test_a_launch_that_fails_ends_the_call_with_an_error():
+    """On a stream whose capture has become invalid every launch is refused on the host: each
+    call says so, and the cache works again once the capture has ended."""
+    c = sa.QuantKVCache(1, 1, 64, 9088)
+    K = normal("fail", (1, 90, 1, 64), BF).cuda()
+    c.append(K, K)
+    out, other = torch.empty_like(K), torch.empty_like(K)
+    want = c.attend(K, add_weight=True)
+    one = c.attend(K[:, :1], add_weight=True)
+    seq, weight = c.seq.clone(), c.weight.clone()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    driver, relaxed = ctypes.CDLL("libcuda.so.1"), 2
+    stream, graph = ctypes.c_void_p(side.cuda_stream), ctypes.c_void_p()
+    assert driver.cuStreamBeginCapture_v2(stream, relaxed) == 0
+    try:
+        assert c.check(stream=side) == sa.SA_ERR_CUDA  # waiting for it makes the capture invalid
+        for call in (lambda: c.append(K, K, stream=side),
+                     lambda: c.read(0, out, other, stream=side),
+                     lambda: c.attend(K, out=out, add_weight=True, stream=side),
+                     lambda: c.attend(K[:, :1], out=out[:, :1], add_weight=True, stream=side),
+                     lambda: c.attend(K[:, :30], out=out[:, :30], add_weight=True, stream=side),
+                     lambda: c.evict(20, stream=side), lambda: c.reset(stream=side)):
+            with pytest.raises(sa.SaError) as e:
+                call()
+            assert e.value.status == sa.SA_ERR_CUDA and "kv4: " in sa.last_error()
+    finally:
+        assert driver.cuStreamEndCapture(stream, ctypes.byref(graph)) != 0
+    torch.cuda.synchronize()
+    assert torch.equal(c.seq, seq) and torch.equal(c.weight[:, :, :90], weight[:, :, :90])
+    assert torch.equal(c.attend(K), want) and torch.equal(c.attend(K[:, :1]), one)
+    c.append(K, K, stream=side)
+    assert c.check(stream=side) == sa.SA_OK and c.seq[0].tolist() == [180]
