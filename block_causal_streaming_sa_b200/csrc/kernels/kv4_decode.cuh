@@ -40,6 +40,12 @@ namespace sa {
 // and below every score.
 constexpr float kNoScore = -3.402823466e38f;
 
+// Blocks an SM of kv4_decode_kernel for 8 nt query rows, by its registers and shared memory;
+// the workspace is laid out for as many.
+__host__ __device__ constexpr int decode_blocks_per_sm(int nt) {
+  return nt == 1 ? 4 : nt == 2 ? 3 : 2;
+}
+
 template <int D, int NT>
 struct DecodeShape {
   static constexpr int kWarps = 4;
@@ -57,7 +63,7 @@ struct DecodeShape {
   static constexpr int kOffSl = kOffQ + (NT > 1 ? kRows * D * 2 : 0);
   static constexpr int kOffBar = kOffSl + kRows * 4;
   static constexpr int kSmem = kOffBar + kWarps * kStages * 8 + 16;
-  static constexpr int kBlocksPerSm = NT == 1 ? 4 : NT == 2 ? 3 : 2;
+  static constexpr int kBlocksPerSm = decode_blocks_per_sm(NT);
 };
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,

@@ -250,8 +250,6 @@ struct AttendPlan {
 constexpr int kFewRows = 64;
 constexpr int kMostSms = 160;  // the workspace covers a grid of any GPU of this kind
 
-int decode_blocks_per_sm(int nt) { return nt == 1 ? 4 : nt == 2 ? 3 : 2; }
-
 AttendPlan plan_attend(const sa_kv4_cache* c, int heads, int T, bool weights) {
   AttendPlan a{};
   if (T == 0) return a;  // nothing runs
@@ -264,7 +262,7 @@ AttendPlan plan_attend(const sa_kv4_cache* c, int heads, int T, bool weights) {
     const int n8 = std::max((rows + 7) / 8, 1);
     a.row_blocks = (n8 + 3) / 4;
     a.nt = (n8 + a.row_blocks - 1) / a.row_blocks;
-    a.blocks = static_cast<long long>(kMostSms) * decode_blocks_per_sm(a.nt);
+    a.blocks = static_cast<long long>(kMostSms) * sa::decode_blocks_per_sm(a.nt);
     const size_t slots = a.blocks + planes * a.row_blocks;
     a.off_o = off;
     off += align_up(slots * 8 * a.nt * D * sizeof(float), 256);
