@@ -130,3 +130,16 @@ def test_rows_that_draw_nothing_from_many_queries_weigh_exactly_zero():
     p.gpu.attend(Q.cuda(), scale=11.3, add_weight=True)
     assert (p.gpu.weight[0, 0, 1:n] == 0).all()
     assert abs(float(p.gpu.weight[0, 0, 0]) - T) <= T * 2.0 ** -21
+
+
+@pytest.mark.parametrize("T", [1, 6, 24, 140])
+@pytest.mark.parametrize("D,dtype,qs", [(128, BF, 40.0), (64, HF, 20.0), (128, BF, 2.0 ** -30)])
+def test_weights_of_large_and_sharp_scores(T, D, dtype, qs):
+    """Keys of very different size: maxima that grow along the rows, probabilities of which
+    most vanish, log-sum-exps in the hundreds."""
+    p = Pair(1, 2, D, 1024, dtype)
+    for i in range(4):
+        p.append(("sharpw", T, i, D), 200, scale=0.3 * 3.0 ** i)
+    e = p.check_attend(("sharpw", T, D, qs), T, 4, q_scale=qs, add_weight=True)
+    p.check_weights(1, e)
+    assert p.gpu.check() == sa.SA_OK
