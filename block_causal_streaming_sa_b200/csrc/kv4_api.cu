@@ -373,36 +373,70 @@ size_t evict_bytes(const sa_kv4_cache* c) {
   return align_up(static_cast<size_t>(c->batch) * c->kv_heads * c->capacity * sizeof(int32_t), 256);
 }
 
-// Blocks that share one head's rows: as many as leave each 4096 rows or more, while
-// all heads' blocks still run at once (two an SM).
-int evict_cluster(const Kv4& c) {
-  int n = 1;
-  while (n < 8 && n * 2 * 4096 <= c.N && 1LL * c.B * c.H * n * 2 <= 2LL * sm_count()) n *= 2;
-  return n;
-}
+constexpr int kMostKeys = 40960;  // keys in an eviction block's shared memory (160 KB)
 
 template <int D>
-cudaError_t launch_evict(sa::Kv4EvictParams p, cudaStream_t s) {
-  constexpr int kMostKeys = 40960;  // 160 KB
-  const int cluster = evict_cluster(p.c);
-  const int per_block = ((p.c.N + cluster * 32 - 1) / (cluster * 32) + 31) / 32 * 32 * 32;
-  p.smem_keys = std::min(per_block, kMostKeys);
-  if (!allow_smem<sa::kv4_evict_kernel<D>>(sa::kEvictFixedSmem + kMostKeys * 4))
-    return cudaErrorInvalidValue;
+cudaLaunchConfig_t evict_config(dim3 grid, int keys, cudaLaunchAttribute (&at)[2]) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(cluster, p.c.H, p.c.B);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(1024);
-  cfg.dynamicSmemBytes = sa::kEvictFixedSmem + p.smem_keys * 4;
-  cfg.stream = s;
-  cudaLaunchAttribute at[2];
+  cfg.dynamicSmemBytes = sa::kEvictFixedSmem + keys * 4;
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = cluster;
+  at[0].val.clusterDim.x = grid.x;
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
   at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 2;
+  return cfg;
+}
+
+// Clusters of `n` eviction blocks that run at once on the current device: one block an SM (its
+// threads fill the registers), and a cluster within a group of SMs that does not divide by
+// it, so the device is asked (once a size).
+template <int D>
+int evict_clusters_at_once(int n) {
+  static std::atomic<int> known[kMaxDevices][4];
+  int dev = 0, count = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+  std::atomic<int>& slot = known[dev][n == 8 ? 3 : n / 2];
+  if ((count = slot.load(std::memory_order_relaxed)) > 0) return count;
+  cudaLaunchAttribute at[2];
+  const cudaLaunchConfig_t cfg = evict_config<D>(dim3(n, 1, 1), kMostKeys, at);
+  if (cudaOccupancyMaxActiveClusters(&count, sa::kv4_evict_kernel<D>, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return sm_count() / n;
+  }
+  slot.store(count, std::memory_order_relaxed);
+  return count;
+}
+
+// Blocks that share one head's rows: as many as leave each 4096 rows or more while all heads
+// still run at once, and in any case enough for the keys to fit their shared memory. Heads x
+// rows, us with this rule and with the next larger (smaller) cluster: 32 x 32768 31 (65, 46),
+// 64 x 32768 61 (73, 93), 16 x 65536 48 (61, 81), 96 x 32768 100 (115), 148 x 131072 554
+// (607, 731).
+template <int D>
+int evict_cluster(const Kv4& c) {
+  int n = 1;
+  while (n < 8 &&
+         (c.N > n * kMostKeys ||
+          (n * 2 * 4096 <= c.N && 1LL * c.B * c.H <= evict_clusters_at_once<D>(n * 2))))
+    n *= 2;
+  return n;
+}
+
+template <int D>
+cudaError_t launch_evict(sa::Kv4EvictParams p, cudaStream_t s) {
+  if (!allow_smem<sa::kv4_evict_kernel<D>>(sa::kEvictFixedSmem + kMostKeys * 4))
+    return cudaErrorInvalidConfiguration;
+  const int cluster = evict_cluster<D>(p.c);
+  const int per_block = ((p.c.N + cluster * 32 - 1) / (cluster * 32) + 31) / 32 * 32 * 32;
+  p.smem_keys = std::min(per_block, kMostKeys);
+  cudaLaunchAttribute at[2];
+  cudaLaunchConfig_t cfg = evict_config<D>(dim3(cluster, p.c.H, p.c.B), p.smem_keys, at);
+  cfg.stream = s;
   return cudaLaunchKernelEx(&cfg, sa::kv4_evict_kernel<D>, p);
 }
 

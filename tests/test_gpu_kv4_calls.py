@@ -3,10 +3,12 @@ reason."""
 
 import ctypes
 
+import numpy as np
 import pytest
 import torch
 
 import block_causal_streaming_sa_b200 as sa
+from oracle import kv4
 from test_gpu_kv4 import BF, Pair, normal
 
 pytestmark = pytest.mark.gpu
@@ -93,3 +95,25 @@ def test_a_launch_that_fails_ends_the_call_with_an_error():
     assert torch.equal(c.attend(K), want) and torch.equal(c.attend(K[:, :1]), one)
     c.append(K, K, stream=side)
     assert c.check(stream=side) == sa.SA_OK and c.seq[0].tolist() == [180]
+
+
+@pytest.mark.parametrize("H,n,keep", [(40, 20_000, 15_001), (70, 9000, 8999), (148, 12_000, 7000),
+                                      (150, 45_000, 30_000)])
+def test_evict_many_heads_of_long_rows(H, n, keep):
+    """Heads that share the device in clusters of every size, and rows whose keys do not fit one
+    block's shared memory though every SM has a head."""
+    c = sa.QuantKVCache(1, H, 64, -(-n // 128) * 128)
+    g = torch.Generator(device="cuda").manual_seed(n)
+    K = torch.randn((1, n, H, 64), generator=g, device="cuda").bfloat16()
+    c.append(K, K)
+    w = torch.randint(0, 5000, c.weight.shape, generator=g, device="cuda").float()
+    c.weight.copy_(w)
+    kc = c.k_codes.clone()
+    c.evict(keep, first=7, recent=300)
+    for h in (0, 1, H // 2, H - 1):
+        src = torch.tensor(kv4.rows_after_eviction(w[0, h, :n].cpu().numpy(), np.arange(n), n,
+                                                   keep, 7, 300), device="cuda")
+        assert torch.equal(c.weight[0, h, :keep], w[0, h, src])
+        assert torch.equal(c.k_codes[0, h, :keep], kc[0, h, src])
+        assert torch.equal(c.pos[0, h, :keep], src.int())
+    assert c.seq[0].tolist() == [keep]
