@@ -217,8 +217,11 @@ __global__ void __launch_bounds__(256)
     kv4_stage_kernel(const __grid_constant__ Kv4AttendParams p) {
   constexpr int C = D / 8;  // 16-byte pieces of a row
   const Kv4& c = p.c;
-  begin_early();
+  // In this order: the next kernel takes all of an SM's tensor memory as soon as it begins,
+  // which a kernel in front of this one that lets its successor begin early may still be
+  // about to allocate; each would wait for the other.
   wait_for_previous();
+  begin_early();
   if (static_cast<int>(blockIdx.x) >= p.q_tiles) {
     if (blockIdx.y != 0 || blockIdx.z != 0) return;
     if (static_cast<int>(blockIdx.x) == p.q_tiles) {

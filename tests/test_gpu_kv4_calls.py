@@ -117,3 +117,28 @@ def test_evict_many_heads_of_long_rows(H, n, keep):
         assert torch.equal(c.k_codes[0, h, :keep], kc[0, h, src])
         assert torch.equal(c.pos[0, h, :keep], src.int())
     assert c.seq[0].tolist() == [keep]
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_row_attention_between_library_matrix_products(D):
+    """Attention of many rows, with weights, in a stream full of matrix products of another
+    library, without a pause: the bits are those of calls that wait."""
+    p = Pair(1, 4, D, 2048)
+    p.append(("mix", D), 2000)
+    Q = normal(("mixq", D), (1, 300, 8, D), BF).cuda()
+    a = torch.randn((2048, 2048), device="cuda").bfloat16()
+    p.gpu.weight.zero_()
+    lse = torch.empty((1, 8, 300), device="cuda")
+    want = p.gpu.attend(Q, lse=lse, add_weight=True)
+    weight, prod = p.gpu.weight.clone(), a @ a
+    torch.cuda.synchronize()
+    for _ in range(20):
+        p.gpu.weight.zero_()
+        x = a @ a
+        out = p.gpu.attend(Q, add_weight=True)
+        y = a @ a
+        again = p.gpu.attend(Q)
+        assert torch.equal(out, want) and torch.equal(again, want)
+        assert torch.equal(x, prod) and torch.equal(y, prod)
+        assert torch.equal(p.gpu.weight[:, :, :2000], weight[:, :, :2000])
+    assert p.gpu.check() == sa.SA_OK
