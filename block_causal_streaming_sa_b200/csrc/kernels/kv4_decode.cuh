@@ -29,7 +29,9 @@
 //
 // Measured: 4 x 131071 rows, 8 heads, D 128, 8 query rows: 125 us, 4.8 TB/s (the copies
 // alone, without arithmetic, 91 us; the rest is unpacking at the 1.3 GHz held under
-// this load). 700 rows, 8 heads: 10 us, launches and dependent loads.
+// this load). 700 rows, 8 heads: 10 us, launches and dependent loads. With 20 query rows
+// (8 sequences of up to 8000 rows, 8 heads, D 64: 23 us) it is latency: eight warps an SM, whose
+// registers allow no more, fill 41 % of the issue slots and 24 % of the matrix unit.
 #pragma once
 
 #include "kv4_params.cuh"

@@ -26,9 +26,10 @@ class QuantKVCache:
     (fp32) [B, Hk, N], ``seq`` (int32 [4, B]: rows held, rows appended in all, rows of the
     last append, rows appended since the last eviction) and ``status`` (int32 [4]).
 
-    One workspace serves every call; calls on one cache must be ordered (one stream, or
-    events). Before capturing a graph make one call of the same shape, so that the
-    workspace is there.
+    One workspace serves every call; calls on one cache, replays of captured ones among
+    them, must be ordered (one stream, or events). Before capturing a graph make one call
+    of the same shape, so that the workspace is there; the object must live as long as
+    the graphs captured from its calls.
     """
 
     def __init__(self, batch, kv_heads, head_dim, capacity, device=None):

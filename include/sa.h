@@ -513,10 +513,14 @@ SA_API int sa_kv4_read(const sa_kv4_cache* c, int first, const sa_rows* K, const
  * natural log of the sum of exp of the scaled scores, or NULL; with it the result
  * merges with an attention over other keys. A query that sees no row gets O = 0,
  * lse = -inf.
+ * O overlaps neither Q nor the cache nor lse. A query that is not finite gets O and lse
+ * NaN, and so do the weights of the rows it sees; all else stays as without it. (Where
+ * every score it has is -inf it counts as one that sees no row.)
  * add_weight != 0 adds to weight[b, k, j], for every row j, the sum of the softmax
  * probabilities that the sequence's queries of KV head k's group gave it.
  * Scores, softmax statistics and sums are fp32; Q enters the products as fp16
- * after a scaling of its row by a power of two, P as fp16, K and V exactly.
+ * after a scaling of its row by a power of two, P as fp16 with the row's largest at 2^10
+ * or above (so a row down to 2^-24 of it keeps its bits), K and V exactly.
  * Workspace: sa_kv4_attend_bytes(...) bytes of device memory, 256-byte aligned,
  * contents free before and after; calls that share it must be ordered. Results do
  * not depend on timing: repeated calls give the same bits. */
