@@ -162,7 +162,7 @@ int check_workspace(const void* ws, size_t bytes, size_t need, int device) {
 // itself waits until that one has finished (wait_for_previous, in every block).
 template <typename... P, typename... A>
 cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
-                  A... args) {
+                         A... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = block;
@@ -420,10 +420,14 @@ int evict_clusters_at_once(int n) {
 template <int D>
 int evict_cluster(const Kv4& c) {
   int n = 1;
-  while (n < 8 &&
-         (c.N > n * kMostKeys ||
-          (n * 2 * 4096 <= c.N && 1LL * c.B * c.H <= evict_clusters_at_once<D>(n * 2))))
+  while (n < 8) {
+    const int at_once = evict_clusters_at_once<D>(n * 2);
+    const bool keys_fit = c.N <= n * kMostKeys;
+    if (at_once < 1 ||  // (part of a device may hold none; keys that do not fit are read again)
+        (keys_fit && (n * 2 * 4096 > c.N || 1LL * c.B * c.H > at_once)))
+      break;
     n *= 2;
+  }
   return n;
 }
 

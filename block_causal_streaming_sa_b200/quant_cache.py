@@ -125,7 +125,7 @@ class QuantKVCache:
         """(pointer, bytes) of a workspace of at least `nbytes()`. One that became too small
         stays allocated: a captured graph, or a call under way on another stream, may use it.
         Each is at least twice the one before, so all together are less than twice the last.
-        None for a call that needs none, or is refused for its sizes (the library says why)."""
+        (0, 0) for a call that needs none, or is refused for its sizes (the library says why)."""
         need = self._sizes.get(key)
         if need is None:
             need = self._sizes[key] = nbytes()
